@@ -1,4 +1,5 @@
-"""ctypes binding of ``libinvrope.so`` (the C ABI declared in ``include/invrope.h``).
+"""ctypes binding of ``libinvrope.so`` (the C ABI declared in ``include/invrope.h``
+and ``include/latent_attn.h``).
 
 Argument marshalling only: each function checks that torch tensors have the
 dtype / device / layout the C ABI expects, allocates outputs with torch when
@@ -27,7 +28,7 @@ INVROPE_ERR_WORKSPACE = 3
 INVROPE_ERR_CUDA = 4
 INVROPE_ERR_DEVICE = 5
 
-# name -> (restype, argtypes); mirrors include/invrope.h
+# name -> (restype, argtypes); mirrors include/invrope.h and include/latent_attn.h
 _SIGNATURES = {
     "invrope_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "invrope_last_cuda_error": (ctypes.c_int, []),
@@ -67,7 +68,29 @@ _SIGNATURES = {
     "invrope_take_device_fault": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int)]),
     "invrope_watchdog_selftest": (ctypes.c_int, [ctypes.c_int64, ctypes.POINTER(ctypes.c_int)]),
     "invrope_debug_occupy_next_slot": (ctypes.c_int, [ctypes.c_int, ctypes.c_ulonglong]),
+    "kv_latent_row_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    "kv_latent_write": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+        ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "kv_latent_read": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+        ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "latent_attn_workspace_bytes": (ctypes.c_size_t, [
+        ctypes.c_int64, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int]),
+    "latent_attn_decode": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_size_t,
+        ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+        ctypes.c_int64, ctypes.c_int, ctypes.c_int64, ctypes.c_double, ctypes.c_void_p]),
+    "latent_attn_sparse": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_size_t,
+        ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+        ctypes.c_int64, ctypes.c_int64, ctypes.c_double, ctypes.c_void_p]),
 }
+
+KV_LATENT_BF16 = 0
+KV_LATENT_E4M3 = 1
 
 INVROPE_WATCHDOG_SELFTEST_CODE = 0x60A
 INVROPE_FAULT_SCHED_BUSY_FWD = 0x5C1
@@ -127,6 +150,15 @@ def _need(t, name, dtype, ndim):
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor that belongs to ``stream`` (None: the current
+    one): its memory is free on the stream the kernels write it on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def invrope_postmix_fwd(O, M, pos0: int, nope: int, pe: int, theta: float = 10000.0,
@@ -303,6 +335,158 @@ def kv_idx_local_to_global_i64(idx, sq: int, seqlen_kv: int, out=None, stream=No
                                           int(seqlen_kv), _stream_handle(idx.device, stream))
     _check(st, "kv_idx_local_to_global_i64")
     return out
+
+
+def kv_latent_row_bytes(nope: int, pe: int, fmt: int) -> int:
+    """Bytes of one cache row (0 if the shape is invalid); ``fmt`` is
+    ``KV_LATENT_BF16`` or ``KV_LATENT_E4M3``."""
+    return int(lib().kv_latent_row_bytes(int(nope), int(pe), int(fmt)))
+
+
+def kv_latent_empty(num_pages: int, page_size: int, nope: int, pe: int, fmt: int = KV_LATENT_BF16, device="cuda"):
+    """A cache of ``num_pages`` pages: bf16 ``[num_pages, page_size, nope+pe]``,
+    or uint8 ``[num_pages, page_size, row bytes]`` for ``KV_LATENT_E4M3``.
+    Its contents are undefined until they are written."""
+    nbytes = kv_latent_row_bytes(nope, pe, fmt)
+    if nbytes == 0:
+        raise ValueError(f"no cache row for nope={nope}, pe={pe}, fmt={fmt}")
+    if fmt == KV_LATENT_E4M3:
+        return torch.empty(num_pages, page_size, nbytes, dtype=torch.uint8, device=device)
+    return torch.empty(num_pages, page_size, nbytes // 2, dtype=torch.bfloat16, device=device)
+
+
+def _cache(cache, nope, pe):
+    """Check a cache tensor against the channel split; returns its format. The
+    dtype tells it: bf16 rows are the values, uint8 rows the e4m3 layout."""
+    if not isinstance(cache, torch.Tensor):
+        raise TypeError("cache must be a torch.Tensor")
+    if cache.dtype == torch.bfloat16:
+        fmt, width = KV_LATENT_BF16, nope + pe
+    else:
+        fmt, width = KV_LATENT_E4M3, kv_latent_row_bytes(nope, pe, KV_LATENT_E4M3)
+    _need(cache, "cache", torch.uint8 if fmt == KV_LATENT_E4M3 else torch.bfloat16, 3)
+    if width and cache.shape[2] != width:  # width 0: the library says why the split is refused
+        raise ValueError(f"cache rows must be {width} wide for nope={nope}, pe={pe}, got {cache.shape[2]}")
+    return fmt
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def kv_latent_write(cache, x, slots, nope: int, pe: int, stream=None):
+    """``cache[slots[i]] = x[i]`` for bf16 vectors ``x`` [n, nope+pe] and int32
+    ``slots`` [n] (slot = page * page_size + place in the page), quantising them
+    where the cache is 8-bit; slots out of range store nothing. Returns ``cache``."""
+    fmt = _cache(cache, nope, pe)
+    _need(x, "x", torch.bfloat16, 2)
+    _need(slots, "slots", torch.int32, 1)
+    n = x.shape[0]
+    if x.shape[1] != nope + pe or slots.shape[0] != n:
+        raise ValueError(f"x must be [n, {nope + pe}] and slots [n]")
+    _same_device(cache.device, x=x, slots=slots)
+    st = lib().kv_latent_write(x.data_ptr(), slots.data_ptr(), cache.data_ptr(), n, cache.shape[0] * cache.shape[1],
+                               nope, pe, fmt, _stream_handle(cache.device, stream))
+    _check(st, "kv_latent_write")
+    return cache
+
+
+def kv_latent_read(cache, slots, nope: int, pe: int, out=None, stream=None):
+    """The bf16 vectors [n, nope+pe] that the cache holds at int32 ``slots`` [n]
+    (zeros for a slot out of range)."""
+    fmt = _cache(cache, nope, pe)
+    _need(slots, "slots", torch.int32, 1)
+    n = slots.shape[0]
+    if out is None:
+        out = _empty((n, nope + pe), torch.bfloat16, cache.device, stream)
+    else:
+        _need(out, "out", torch.bfloat16, 2)
+        if tuple(out.shape) != (n, nope + pe):
+            raise ValueError(f"out must be [{n}, {nope + pe}]")
+    _same_device(cache.device, slots=slots, out=out)
+    st = lib().kv_latent_read(cache.data_ptr(), slots.data_ptr(), out.data_ptr(), n, cache.shape[0] * cache.shape[1],
+                              nope, pe, fmt, _stream_handle(cache.device, stream))
+    _check(st, "kv_latent_read")
+    return out
+
+
+def latent_attn_workspace_bytes(rows: int, nh: int, max_tokens: int, nope: int, pe: int) -> int:
+    """Workspace bytes the attention needs on the current device (0: none)."""
+    return int(lib().latent_attn_workspace_bytes(int(rows), int(nh), int(max_tokens), int(nope), int(pe)))
+
+
+def _attn_io(q, cache, nope, pe, max_tokens, O, lse, workspace, stream, **tables):
+    """Checks and outputs common to the two attention calls."""
+    fmt = _cache(cache, nope, pe)
+    _need(q, "q", torch.bfloat16, 3)
+    rows, nh, d = q.shape
+    if d != nope + pe:
+        raise ValueError(f"q must be [rows, nh, {nope + pe}]")
+    if O is None:
+        O = _empty(q.shape, torch.bfloat16, q.device, stream)
+    else:
+        _need(O, "O", torch.bfloat16, 3)
+        if O.shape != q.shape:
+            raise ValueError("O must have q's shape")
+    if lse is None:
+        lse = _empty((rows, nh), torch.float32, q.device, stream)
+    else:
+        _need(lse, "lse", torch.float32, 2)
+        if tuple(lse.shape) != (rows, nh):
+            raise ValueError(f"lse must be [{rows}, {nh}]")
+    if workspace is None:
+        nbytes = lib().latent_attn_workspace_bytes(rows, nh, max_tokens, nope, pe)
+        workspace = _empty((nbytes,), torch.uint8, q.device, stream) if nbytes else None
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    else:
+        tables["workspace"] = workspace
+    _same_device(q.device, cache=cache, O=O, lse=lse, **tables)
+    ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return fmt, O, lse, ws, workspace
+
+
+def latent_attn_decode(q, cache, page_table, lens, nope: int, pe: int, scale=None, O=None, lse=None,
+                       workspace=None, stream=None):
+    """Attention of one new token a row over its pages of the latent cache, which
+    are keys and values of every head: ``q`` bf16 [rows, nh, nope+pe],
+    ``page_table`` int32 [rows, max_pages], ``lens`` int32 [rows] tokens a row.
+    ``scale`` defaults to ``(nope+pe) ** -0.5``. Returns ``(O bf16, lse fp32 [rows, nh])``;
+    a row with nothing to attend to gives zeros and -inf."""
+    _need(page_table, "page_table", torch.int32, 2)
+    _need(lens, "lens", torch.int32, 1)
+    max_pages = page_table.shape[1]
+    fmt, O, lse, ws, workspace = _attn_io(q, cache, nope, pe, max_pages * cache.shape[1], O, lse, workspace,
+                                          stream, page_table=page_table, lens=lens)
+    rows, nh, d = q.shape
+    if page_table.shape[0] != rows or lens.shape[0] != rows:
+        raise ValueError(f"page_table must be [{rows}, max_pages] and lens [{rows}]")
+    handle = _stream_handle(q.device, stream)
+    st = lib().latent_attn_decode(q.data_ptr(), cache.data_ptr(), page_table.data_ptr(), lens.data_ptr(), O.data_ptr(),
+                                  lse.data_ptr(), ws[0], ws[1], rows, nh, nope, pe, fmt, cache.shape[0],
+                                  cache.shape[1], max_pages, d ** -0.5 if scale is None else float(scale), handle)
+    _check(st, "latent_attn_decode")
+    return O, lse
+
+
+def latent_attn_sparse(q, cache, idx, nope: int, pe: int, scale=None, O=None, lse=None, workspace=None, stream=None):
+    """The same attention over the cache slots that ``idx`` int32 [rows, topk]
+    selects for each row (the flat-global table of :func:`kv_idx_local_to_global`;
+    entries out of range, such as -1 padding, are left out)."""
+    _need(idx, "idx", torch.int32, 2)
+    rows, topk = idx.shape
+    fmt, O, lse, ws, workspace = _attn_io(q, cache, nope, pe, topk, O, lse, workspace, stream, idx=idx)
+    if q.shape[0] != rows:
+        raise ValueError("idx must have a row for each of q's")
+    nh, d = q.shape[1:]
+    handle = _stream_handle(q.device, stream)
+    st = lib().latent_attn_sparse(q.data_ptr(), cache.data_ptr(), idx.data_ptr(), O.data_ptr(), lse.data_ptr(), ws[0],
+                                  ws[1], rows, nh, nope, pe, fmt, cache.shape[0] * cache.shape[1], topk,
+                                  d ** -0.5 if scale is None else float(scale), handle)
+    _check(st, "latent_attn_sparse")
+    return O, lse
 
 
 def invrope_take_device_fault() -> int:

@@ -25,7 +25,7 @@ LIB_PATH = os.path.join(PKG, "libinvrope.so")
 DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(PKG, "libinvrope_debug.so")
 
-SOURCES = ["postmix.cu", "remap.cu", "api.cpp", "noalloc.cu"]
+SOURCES = ["postmix.cu", "remap.cu", "api.cpp", "noalloc.cu", "latent_cache.cu", "latent_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

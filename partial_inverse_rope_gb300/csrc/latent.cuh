@@ -1,0 +1,69 @@
+// Row layout of the latent cache (include/latent_attn.h) and the conversion of
+// e4m3 codes with power-of-two scales to bf16, shared by the cache's and the
+// attention's kernels.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+
+#include "latent_attn.h"
+
+namespace invrope {
+namespace latent {
+
+constexpr int kGroup = 64;   // channels that share a scale
+constexpr int kMaxD = 512;
+constexpr int kEMin = -120;  // smallest scale: 2^-120 * 2^-9 (least e4m3 step) is still exact in bf16
+constexpr int kEMax = 119;   // largest: 448 * 2^119 is bf16's range, 448 * 2^120 is not
+
+struct RowLayout {
+  int nope, pe, d;
+  int row_bytes;
+  int scale_off;  // byte offset of the scales (e4m3 rows)
+};
+
+// Returns INVROPE_OK and fills *l, or an error status.
+inline int row_layout(int nope, int pe, int fmt, RowLayout* l) {
+  if (fmt != KV_LATENT_BF16 && fmt != KV_LATENT_E4M3) return INVROPE_ERR_INVALID_ARG;
+  if (nope < 0 || pe < 0 || nope > (1 << 20) || pe > (1 << 20)) return INVROPE_ERR_INVALID_ARG;
+  const int d = nope + pe;
+  if (d < 8 || d % 8) return INVROPE_ERR_INVALID_ARG;
+  if (fmt == KV_LATENT_E4M3 && (nope < 16 || nope % 16 || pe % 8)) return INVROPE_ERR_INVALID_ARG;
+  if (d > kMaxD) return INVROPE_ERR_UNSUPPORTED;
+  l->nope = nope;
+  l->pe = pe;
+  l->d = d;
+  l->scale_off = nope + 2 * pe;
+  l->row_bytes = fmt == KV_LATENT_BF16 ? 2 * d : (l->scale_off + (nope + kGroup - 1) / kGroup + 15) / 16 * 16;
+  return INVROPE_OK;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// A scale byte as two equal bf16 values 2^(byte-127); 255 gives NaN. (The byte
+// is bf16's exponent field; the writer keeps it within 7..246, or 255.)
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t byte) {
+  const uint32_t h = byte == 255u ? 0x7FC0u : byte << 7;
+  return h | (h << 16);
+}
+
+// Four e4m3 codes -> four bf16 values times their group's scale. A code's
+// exponent and mantissa bits, moved into bf16's fields, read as value * 2^-120
+// (e4m3's bias is 7, bf16's 127; e4m3 subnormals become bf16 subnormals), so
+// one exact product with 2^120 restores the value and a second one scales it:
+// 4 integer operations and 4 products for 4 values.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t scale2, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0u, 0x1404u), b = __byte_perm(w, 0u, 0x3424u);
+  const uint32_t k = 0x7B807B80u;  // 2^120 twice
+  lo = mul_bf16x2(mul_bf16x2((a & 0x80008000u) | ((a & 0x7F007F00u) >> 4), k), scale2);
+  hi = mul_bf16x2(mul_bf16x2((b & 0x80008000u) | ((b & 0x7F007F00u) >> 4), k), scale2);
+}
+
+}  // namespace latent
+}  // namespace invrope
