@@ -62,6 +62,9 @@ int slot_reset_all(SlotRing& ring, const void* symbol, int device);
 // Read and clear the remap kernel's fault word on the current device.
 int take_remap_fault(unsigned int* code);
 
+// Read and clear the latent attention's fault word on the current device.
+int take_latent_fault(unsigned int* code);
+
 // Reset the forward's and the remap's slot arrays on `device`.
 int reset_postmix_sched(int device);
 int reset_remap_sched(int device);

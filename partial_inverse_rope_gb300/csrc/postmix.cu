@@ -2320,13 +2320,13 @@ extern "C" int invrope_take_device_fault(int* fault) {
   cudaError_t err = cudaGetDevice(&device);
   if (err != cudaSuccess) return cuda_fail(err);
   if ((err = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(err);
-  unsigned v = 0, vr = 0;
+  unsigned v = 0, vr = 0, va = 0;
   if ((err = cudaMemcpyFromSymbol(&v, g_fault_code, sizeof(v))) != cudaSuccess) return cuda_fail(err);
   const unsigned zero = 0;
   if ((err = cudaMemcpyToSymbol(g_fault_code, &zero, sizeof(zero))) != cudaSuccess) return cuda_fail(err);
   int st = take_remap_fault(&vr);
-  if (st != INVROPE_OK) return st;
-  if (v == 0) v = vr;
+  if (st != INVROPE_OK || (st = take_latent_fault(&va)) != INVROPE_OK) return st;
+  if (v == 0) v = vr != 0 ? vr : va;
   // After a fault a launch may have left a work-counter slot held (its
   // blocks that found the slot busy never release it): nothing runs on the
   // device now, so every slot is returned to the free state.
