@@ -53,16 +53,22 @@ __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t byte) {
   return h | (h << 16);
 }
 
-// Four e4m3 codes -> four bf16 values times their group's scale. A code's
-// exponent and mantissa bits, moved into bf16's fields, read as value * 2^-120
-// (e4m3's bias is 7, bf16's 127; e4m3 subnormals become bf16 subnormals), so
-// one exact product with 2^120 restores the value and a second one scales it:
-// 4 integer operations and 4 products for 4 values.
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t scale2, uint32_t& lo, uint32_t& hi) {
+// Four e4m3 codes -> four bf16 values. A code's exponent and mantissa bits,
+// moved into bf16's fields, read as value * 2^-120 (e4m3's bias is 7, bf16's
+// 127; e4m3 subnormals become bf16 subnormals); the product with `factor`, a
+// power of two twice, is exact.
+__device__ __forceinline__ void e4m3x4_times(uint32_t w, uint32_t factor, uint32_t& lo, uint32_t& hi) {
   const uint32_t a = __byte_perm(w, 0u, 0x1404u), b = __byte_perm(w, 0u, 0x3424u);
-  const uint32_t k = 0x7B807B80u;  // 2^120 twice
-  lo = mul_bf16x2(mul_bf16x2((a & 0x80008000u) | ((a & 0x7F007F00u) >> 4), k), scale2);
-  hi = mul_bf16x2(mul_bf16x2((b & 0x80008000u) | ((b & 0x7F007F00u) >> 4), k), scale2);
+  lo = mul_bf16x2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), factor);
+  hi = mul_bf16x2((b & 0x80008000u) | ((b >> 4) & 0x07F007F0u), factor);
+}
+
+// The same times the group's scale: 2^120 and the scale, which together may
+// have no bf16 value, one after the other.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t scale2, uint32_t& lo, uint32_t& hi) {
+  e4m3x4_times(w, 0x7B807B80u, lo, hi);
+  lo = mul_bf16x2(lo, scale2);
+  hi = mul_bf16x2(hi, scale2);
 }
 
 }  // namespace latent

@@ -16,9 +16,14 @@
 // over several blocks leaves one partial (accumulators, reference and sum in
 // fp32) for each, which latent_join_kernel adds up in a fixed order.
 //
-// Warps: 0-3 softmax and output (TMEM lanes), 4 MMA issue, 5 queries (TMA),
-// 6-13 cache rows: global loads one tile ahead in registers, e4m3 codes
-// converted on the way to shared memory.
+// Warps: 0-3 softmax and output (TMEM lanes), 4 queries (TMA) and S, 5 O^T (a
+// warp each: either product goes out as soon as what it needs is there, so a
+// late tile does not hold up the one that frees its stages), 6 the tokens'
+// cache slots, from 7 on cache rows. A loading warp takes one
+// (tile, 128-channel block) at a time. bf16 rows go straight to shared memory
+// (cp.async, as far ahead as the ring is free). e4m3 rows are held in registers
+// while in flight (the ring of bf16 tiles leaves no shared memory for them),
+// one block a warp, and converted on the way.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -42,16 +47,20 @@ using latent::RowLayout;
 
 constexpr int kTile = 64;        // tokens per tile
 constexpr int kBlock = 128;      // channels per stage of the ring
-constexpr int kMaxBlocks = latent::kMaxD / kBlock;
 constexpr int kStages = 9;       // two tiles of 512 channels and one stage more
 constexpr int kStageBytes = kTile * kBlock * 2;
 constexpr int kHalf = kTile * 128;       // one 64-channel half of a stage
-constexpr int kMaskRing = 16;    // tiles whose token masks are kept (the ring holds at most 9)
+constexpr int kSlotRing = 4;     // tiles whose slots are looked up ahead of their loads
+constexpr int kMaskRing = 32;    // tiles whose token masks are kept: those of both rings, at most 14
 constexpr int kOverhead = 2;     // what a row costs beside its tiles, in tiles
 constexpr int kMinUnits = 4;     // units of the line a thread block takes at least
 
 constexpr int kSoftmaxThreads = 128;
-constexpr int kMmaWarp = 4, kQueryWarp = 5, kLoadWarp = 6, kLoadWarps = 8;
+constexpr int kScoreWarp = 4, kValueWarp = 5, kTokenWarp = 6, kLoadWarp = 7;
+// Loading warps take blocks in turn. At most kStages and, over all blocks of a
+// tile, kSlotRing tiles apart: a parity then tells the phase a warp waits for
+// from the one before the one before.
+constexpr int kLoadWarps = kStages;
 constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
 
 // shared memory, from a 1024-byte boundary
@@ -61,24 +70,34 @@ constexpr int kOffP = kOffRing + kStages * kStageBytes;     // 2 x [64 heads][64
 constexpr int kOffCtl = kOffP + 2 * 64 * 128;
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], drained;
-  uint32_t mask[kMaskRing][4];  // a byte for 4 tokens, bit k: token 4 * byte + k is attended to
+  uint64_t slots_full[kSlotRing], slots_empty[kSlotRing];
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], drained[2];
+  uint64_t mask[kMaskRing];     // bit t: token t of the tile is attended to
+  int slot[kSlotRing][kTile];   // -1: left out; kNoTile: no more tiles
   float factor[2][64];
   float inv[64];
   int64_t sums[kThreads / 32];
-  int64_t total, base;
+  int64_t base;
   int row;
   int abort;
   uint32_t tmem;
 };
-constexpr int kSmem = kOffCtl + static_cast<int>(sizeof(Ctl)) + 1024;
+constexpr int kNoTile = -2;
+constexpr int kSmem = kOffCtl + static_cast<int>(sizeof(Ctl));
 static_assert(kSmem <= 227 * 1024, "shared memory of one thread block");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 256;  // two S tiles of 64 columns; O^T takes 64 columns a channel block from 0
 
 // fault codes: role in bits 8-11, barrier kind in bits 0-7
-enum : unsigned { kFaultLoad = 0xA01, kFaultMma = 0xB01, kFaultQuery = 0xC01, kFaultSoftmax = 0xD01 };
+enum : unsigned {
+  kFaultLoad = 0xA01,
+  kFaultScore = 0xB01,
+  kFaultValue = 0xC01,
+  kFaultSoftmax = 0xD01,
+  kFaultToken = 0xE01,
+  kFaultSmem = 0xF01  // shared memory does not begin on a 1024-byte boundary
+};
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct AttnParams {
@@ -93,7 +112,8 @@ struct AttnParams {
   float* part;           // [slots][heads of a tile][d]
   float2* part_ml;       // [slots][heads of a tile] (reference, sum)
   int4* split;           // [blocks] (pieces, row, head tile, 0); pieces = 0: none begins in the block
-  int64_t rows, width, num_slots, num_pages;
+  int64_t rows, width, num_slots;
+  int num_pages;         // entries of an index table are pages of one slot
   int nh, head_tiles, tile_heads, page_size;
   float scale_log2;      // scale * log2(e)
   RowLayout l;
@@ -132,15 +152,24 @@ __device__ __forceinline__ int tiles_of(const AttnParams& p, int64_t r) {
   return static_cast<int>((static_cast<unsigned>(tokens_of(p, r)) + kTile - 1) / kTile);
 }
 
-// The cache slot of token t of row r, or -1 when it is left out.
-__device__ __forceinline__ int slot_of(const AttnParams& p, int64_t r, int t) {
-  if (!p.lens) {
-    const int s = __ldg(p.table + r * p.width + t);
-    return s >= 0 && s < p.num_slots ? s : -1;
-  }
+// Token t of row r as its table entry (a page, or a slot as a page of one) and
+// place in the page; slot_of turns them into a cache slot, or -1 when the token
+// is left out. Apart, so that an entry's load is not waited for where it is issued.
+struct Ref {
+  int entry, place;
+};
+__device__ __forceinline__ int load_entry(const int32_t* at) {  // volatile: stays where it is issued
+  int v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(at));
+  return v;
+}
+__device__ __forceinline__ Ref ref_of(const AttnParams& p, int64_t r, int t) {
+  if (!p.lens) return Ref{load_entry(p.table + r * p.width + t), 0};
   const int pg = static_cast<int>(static_cast<unsigned>(t) / static_cast<unsigned>(p.page_size));
-  const int g = __ldg(p.table + r * p.width + pg);
-  return g >= 0 && g < p.num_pages ? g * p.page_size + (t - pg * p.page_size) : -1;
+  return Ref{load_entry(p.table + r * p.width + pg), t - pg * p.page_size};
+}
+__device__ __forceinline__ int slot_of(const AttnParams& p, const Ref& x) {
+  return x.entry >= 0 && x.entry < p.num_pages ? x.entry * p.page_size + x.place : -1;
 }
 
 // First unit of thread block c's run of a line of `total` units cut into n runs,
@@ -243,65 +272,142 @@ __device__ __forceinline__ uint4 load_16(const char* at) {
 
 __device__ __forceinline__ void store_16(uint32_t at, const uint4& v) { ptx::st_shared_v4(at, v.x, v.y, v.z, v.w); }
 
-// One loading thread's share of a tile: tokens tok and tok + 32, and of each
-// 128-channel block the 16 channels that thread j of 8 takes: units j and j + 8
-// of 8 channels (bf16 rows), or the 16 channels from 16 j on (e4m3 rows).
-struct Raw {
-  uint4 a[kMaxBlocks][2], b[kMaxBlocks][2];
-};
+__device__ __forceinline__ uint32_t unit_addr(uint32_t stage, int tok, int unit) {  // 8 channels a unit
+  return stage + (unit >> 3) * kHalf + tok * 128 + (((unit & 7) ^ (tok & 7)) << 4);
+}
 
-// Loads block b of the tile whose slots are given; what is not there reads 0.
-template <bool E4M3>
-__device__ __forceinline__ void load_block(const AttnParams& p, Raw& raw, int b, int j, const int (&slot)[2]) {
+// 16 bytes global -> shared without a register; zeros where !there.
+__device__ __forceinline__ void copy_16(uint32_t to, const char* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+
+// This thread's arrival on `bar` when its copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Block b of a bf16 tile: a warp's instruction covers 256 bytes of tokens k and
+// 32 + k.
+__device__ __forceinline__ void copy_block(const AttnParams& p, const int* slots, int b, int lane, uint32_t stage) {
+  const int unit = lane & 15, half = lane >> 4, c = b * kBlock + 8 * unit;
+  const bool mine = c < p.l.d;
+  const char* from = p.cache + (mine ? 2 * c : 0);
+  const uint32_t to = stage + (unit >> 3) * kHalf + half * 4096u;
+  const int4* s4 = reinterpret_cast<const int4*>(slots + 32 * half);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const char* row = p.cache + static_cast<int64_t>(slot[k]) * p.l.row_bytes;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    if (!E4M3) {
-      const int c = b * kBlock + 8 * j;
-      raw.a[b][k] = slot[k] >= 0 && c < p.l.d ? load_16(row + 2 * c) : zero;
-      raw.b[b][k] = slot[k] >= 0 && c + 64 < p.l.d ? load_16(row + 2 * c + 128) : zero;
-    } else {
-      const int c = b * kBlock + 16 * j;
-      const int pe = p.l.nope + 2 * (c - p.l.nope);
-      raw.a[b][k] = slot[k] >= 0 && c < p.l.d ? load_16(row + (c < p.l.nope ? c : pe)) : zero;
-      raw.b[b][k] = slot[k] >= 0 && c >= p.l.nope && c + 8 < p.l.d ? load_16(row + pe + 16) : zero;
+  for (int q = 0; q < 8; ++q) {
+    const int4 s = s4[q];
+    const int slot[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = 4 * q + i;
+      const bool there = mine && slot[i] >= 0;
+      copy_16(to + k * 128u + (((unit & 7) ^ (k & 7)) << 4),
+              from + static_cast<int64_t>(there ? slot[i] : 0) * p.l.row_bytes, there);
     }
   }
 }
 
-__device__ __forceinline__ uint32_t unit_addr(uint32_t stage, int tok, int unit) {
-  return stage + (unit >> 3) * kHalf + tok * 128 + (((unit & 7) ^ (tok & 7)) << 4);
+// A warp's share of an e4m3 tile, held in its registers while in flight. Of a
+// block of codes only, the whole block: 8 lanes take a token (16 codes each), 4
+// tokens a step, 16 steps. Of a block with pe channels, 32 tokens: 16 lanes take
+// a token, those past its codes one unit of 8 bf16 values each, 2 tokens a step.
+struct RawUnit {
+  uint4 v[16];
+  uint32_t scales;  // the block's two scale bytes of tokens lane (low half) and lane + 32
+};
+struct UnitShape {
+  int b, codes, units;  // channel block, and its 16-code items and 8-value pe units of a token
+  bool wide;            // with pe channels
+  int first, step;      // this lane's tokens
+  int item;             // and its item of each
+};
+// Units of a tile: the blocks in order, those with pe channels as two.
+__device__ __forceinline__ int units_of(const RowLayout& l, int nblk) {
+  return l.pe > 0 ? 2 * nblk - l.nope / kBlock : nblk;
+}
+__device__ __forceinline__ UnitShape unit_shape(const RowLayout& l, int nblk, int u, int lane) {
+  const int plain = l.pe > 0 ? l.nope / kBlock : nblk;
+  UnitShape q;
+  q.wide = u >= plain;
+  q.b = q.wide ? plain + (u - plain) / 2 : u;
+  const int c0 = q.b * kBlock;
+  q.codes = min(max(l.nope - c0, 0), kBlock) / 16;
+  q.units = q.wide ? max(min(l.d, c0 + kBlock) - max(l.nope, c0), 0) / 8 : 0;
+  q.item = q.wide ? lane & 15 : lane & 7;
+  q.step = q.wide ? 2 : 4;
+  q.first = q.wide ? 32 * ((u - plain) & 1) + (lane >> 4) : lane >> 3;
+  return q;
 }
 
-// Writes block b of a tile into its stage, 128-byte swizzled.
-template <bool E4M3>
-__device__ __forceinline__ void store_block(const AttnParams& p, const Raw& raw, int b, int j, int tok,
-                                            const uint2 (&scales)[2], uint32_t stage) {
+__device__ __forceinline__ void load_unit(const AttnParams& p, RawUnit& raw, const UnitShape& q, const int* slots,
+                                          int lane) {
+  const int c0 = q.b * kBlock;
+  // byte offset in the row of this lane's item
+  const int at = q.item < q.codes ? c0 + 16 * q.item
+                                  : p.l.nope + 2 * max(c0 - p.l.nope, 0) + 16 * (q.item - q.codes);
+  const bool mine = q.item < q.codes + q.units;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int slot = slots[q.first + q.step * k];
+    raw.v[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (mine && slot >= 0) raw.v[k] = load_16(p.cache + static_cast<int64_t>(slot) * p.l.row_bytes + at);
+  }
+  unsigned short two[2] = {0, 0};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int t = tok + 32 * k;
-    if (!E4M3) {
-      store_16(unit_addr(stage, t, j), raw.a[b][k]);
-      store_16(unit_addr(stage, t, j + 8), raw.b[b][k]);
-    } else {
-      uint4 lo = raw.a[b][k], hi = raw.b[b][k];
-      const int c = b * kBlock + 16 * j;
-      if (c < p.l.nope) {
-        const int g = c / latent::kGroup;  // 2b or 2b + 1
-        const uint32_t byte = ((g < 4 ? scales[k].x : scales[k].y) >> (8 * (g & 3))) & 255u;
-        const uint32_t s = latent::scale_bf16x2(byte);
-        const uint4 w = lo;
-        latent::e4m3x4_to_bf16(w.x, s, lo.x, lo.y);
-        latent::e4m3x4_to_bf16(w.y, s, lo.z, lo.w);
-        latent::e4m3x4_to_bf16(w.z, s, hi.x, hi.y);
-        latent::e4m3x4_to_bf16(w.w, s, hi.z, hi.w);
+    const int slot = slots[lane + 32 * k];
+    if (slot >= 0 && q.codes > 0)  // rows end on a 16-byte boundary: two bytes are there even where one group is
+      asm volatile("ld.global.nc.u16 %0, [%1];"
+                   : "=h"(two[k])
+                   : "l"(p.cache + static_cast<int64_t>(slot) * p.l.row_bytes + p.l.scale_off + 2 * q.b));
+  }
+  raw.scales = two[0] | static_cast<uint32_t>(two[1]) << 16;
+}
+
+__device__ __forceinline__ void store_unit(const RowLayout& l, const RawUnit& raw, const UnitShape& q, int lane,
+                                           uint32_t stage) {
+  // 2^(byte - 127) times the 2^120 of the conversion, as one bf16 factor; a
+  // scale of more than 2^7 has no such product and takes two.
+  uint32_t byte[16];
+  bool large = false;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int t = q.first + q.step * k;
+    const uint32_t two = __shfl_sync(0xFFFFFFFFu, raw.scales, t & 31) >> (16 * (t >> 5));
+    byte[k] = (two >> (8 * ((q.item >> 2) & 1))) & 255u;
+    large = large || (byte[k] > 134u && byte[k] != 255u);
+  }
+  large = __any_sync(0xFFFFFFFFu, large && q.item < q.codes);
+  // the first unit of 8 channels in the block that pe lanes write
+  const int pe_unit = max(l.nope - q.b * kBlock, 0) / 8 + q.item - q.codes;
+  const int odd = (q.item >> 2) & 1;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int t = q.first + q.step * k;
+    if (q.item < q.codes) {
+      const uint4 w = raw.v[k];
+      uint4 lo, hi;
+      if (!large) {
+        const uint32_t f = byte[k] == 255u ? 0x7FC0u : (byte[k] + 120u) << 7;
+        const uint32_t f2 = f | f << 16;
+        latent::e4m3x4_times(w.x, f2, lo.x, lo.y);
+        latent::e4m3x4_times(w.y, f2, lo.z, lo.w);
+        latent::e4m3x4_times(w.z, f2, hi.x, hi.y);
+        latent::e4m3x4_times(w.w, f2, hi.z, hi.w);
+      } else {
+        const uint32_t f2 = latent::scale_bf16x2(byte[k]);
+        latent::e4m3x4_to_bf16(w.x, f2, lo.x, lo.y);
+        latent::e4m3x4_to_bf16(w.y, f2, lo.z, lo.w);
+        latent::e4m3x4_to_bf16(w.z, f2, hi.x, hi.y);
+        latent::e4m3x4_to_bf16(w.w, f2, hi.z, hi.w);
       }
-      // threads of the two 64-channel halves write the even and the odd unit
-      // first in turn: 8 threads of a token then cover all 32 banks
-      const int odd = j >> 2;
-      store_16(unit_addr(stage, t, 2 * j + odd), odd ? hi : lo);
-      store_16(unit_addr(stage, t, 2 * j + 1 - odd), odd ? lo : hi);
+      // lanes of the two 64-channel halves write the even and the odd unit
+      // first in turn: 8 lanes of a token then cover all 32 banks
+      store_16(unit_addr(stage, t, 2 * q.item + odd), odd ? hi : lo);
+      store_16(unit_addr(stage, t, 2 * q.item + 1 - odd), odd ? lo : hi);
+    } else if (pe_unit < 16) {  // a pe unit, or zeros behind the last channel
+      store_16(unit_addr(stage, t, pe_unit), raw.v[k]);
     }
   }
 }
@@ -365,31 +471,42 @@ __device__ __forceinline__ bool any_softmax(bool x) {
 
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_constant__ AttnParams p) {
-  extern __shared__ char smem_raw[];
-  const uint32_t base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
-  char* smem = smem_raw + (base - ptx::smem_u32(smem_raw));
+  extern __shared__ __align__(1024) char smem[];
+  const uint32_t base = ptx::smem_u32(smem);
+  if (base & 1023u) {  // never: the declaration asks for it
+    if (threadIdx.x == 0) atomicCAS(&g_latent_fault, 0u, static_cast<unsigned>(kFaultSmem));
+    return;
+  }
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + kOffCtl);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   volatile int* abort_flag = &ctl->abort;
+  const int nblk = (p.l.d + kBlock - 1) / kBlock;
+  const int units = E4M3 ? units_of(p.l, nblk) : nblk;  // loading warps' shares of a tile
+  const int load_warps = min(kLoadWarps, kSlotRing * units);
   const auto bar = [](uint64_t& b) { return ptx::smem_u32(&b); };
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(bar(ctl->full[s]), kLoadWarps);
+      ptx::mbar_init(bar(ctl->full[s]), E4M3 ? 64 : 32);
       ptx::mbar_init(bar(ctl->empty[s]), 1);
+    }
+    for (int i = 0; i < kSlotRing; ++i) {
+      ptx::mbar_init(bar(ctl->slots_full[i]), 1);
+      ptx::mbar_init(bar(ctl->slots_empty[i]), units);
     }
     ptx::mbar_init(bar(ctl->q_full), 1);
     ptx::mbar_init(bar(ctl->q_empty), 1);
     for (int k = 0; k < 2; ++k) {
       ptx::mbar_init(bar(ctl->s_full[k]), 1);
+      ptx::mbar_init(bar(ctl->s_empty[k]), kSoftmaxThreads);
+      ptx::mbar_init(bar(ctl->drained[k]), 1);
       ptx::mbar_init(bar(ctl->p_full[k]), kSoftmaxThreads);
       ptx::mbar_init(bar(ctl->o_done[k]), 1);
     }
-    ptx::mbar_init(bar(ctl->drained), 1);
     ctl->abort = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem), kTmemCols);
     ptx::tmem_relinquish();
   }
@@ -400,10 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-  const int nblk = (p.l.d + kBlock - 1) / kBlock;
   Piece x;
 
-  if (warp < kMmaWarp) {
+  if (warp < kScoreWarp) {
     // ---------------------------------------------------------------- softmax and output
     const int hq = 16 * warp + lane / 4;  // this thread's heads: hq and hq + 8 of the tile
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // TMEM lane field, 32 * warp
@@ -415,24 +531,24 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
       for (int j = x.j0; j < x.j1; ++j, ++g) {
         wait_bar(bar(ctl->s_full[g & 1]), (g >> 1) & 1, abort_flag, kFaultSoftmax);
-        // the tile's masks were written before its stages were filled; its
-        // stages are still full (only this tile's weights let them go)
+        // the tile's mask was written before its stages were filled; they are
+        // still full (only this tile's weights let them go)
         const uint32_t n0 = g * nblk;
         wait_bar(bar(ctl->full[n0 % kStages]), (n0 / kStages) & 1, abort_flag, kFaultSoftmax);
         ptx::tc_fence_after();
         uint32_t r[32];
         tmem_ld_16x64(tmem + kColS + (g & 1) * 64 + lanes, r);
-        const uint32_t* mk = ctl->mask[g % kMaskRing];
-        const uint32_t mk0 = mk[0], mk1 = mk[1], mk2 = mk[2], mk3 = mk[3];
+        const uint64_t mask = ctl->mask[g % kMaskRing];
         ptx::tmem_ld_wait(r);
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(ctl->s_empty[g & 1]));
         float s[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) s[k] = __uint_as_float(r[k]) * p.scale_log2;
-        if ((mk0 & mk1 & mk2 & mk3) != 0x0F0F0F0Fu) {
-          const uint32_t word[4] = {mk0, mk1, mk2, mk3};
+        if (~mask != 0) {
 #pragma unroll
           for (int u = 0; u < 8; ++u) {  // columns 8 u + 2 (lane % 4) and the next
-            const uint32_t bits = word[u >> 1] >> (16 * (u & 1) + 8 * ((lane & 3) >> 1) + 2 * (lane & 1));
+            const uint32_t bits = static_cast<uint32_t>(mask >> (8 * u)) >> (2 * (lane & 3));
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               if (!(bits >> (k & 1) & 1u)) s[4 * u + k] = -INFINITY;
@@ -462,6 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
           if ((lane & 3) == 0) ctl->factor[g & 1][hq + 8 * i] = f;
           ref[i] = m[i] == -INFINITY ? 0.f : m[i];
         }
+        // the weights of two tiles before are read
+        if (g >= 2) wait_bar(bar(ctl->o_done[g & 1]), ((g >> 1) - 1) & 1, abort_flag, kFaultSoftmax);
         const uint32_t pt = base + kOffP + (g & 1) * 8192u;
 #pragma unroll
         for (int u = 0; u < 8; ++u)
@@ -511,7 +629,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
             if (p.lse && h < heads)
               p.lse[out + h] = sum[i] == 0.f ? -INFINITY : (m[i] + log2f(sum[i])) * 0.6931471805599453f;
           } else if (h < heads) {
-            ctl->inv[h] = 1.f;
             p.part_ml[slot * p.tile_heads + h] = make_float2(m[i], sum[i]);
           }
         }
@@ -526,197 +643,237 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       }
       ptx::named_bar_sync(1, kSoftmaxThreads);  // inv is written
       if (x.j1 > x.j0) {
-        // the last tile's product (s_full of that tile stood for the one two
-        // before it, so the parity is of this phase or the one before)
+        // the last tile's product (the one two before it is known to be in,
+        // so the parity is of this phase or the one before)
         wait_bar(bar(ctl->o_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, kFaultSoftmax);
         ptx::tc_fence_after();
       }
-      for (int b = 0; b < nblk; ++b) {
-        const int c = b * kBlock + 32 * warp + lane;
-        for (int h1 = 0; h1 < heads; h1 += 16) {
-          uint32_t v[16] = {};
-          if (x.j1 > x.j0) tmem_ld_x16(tmem + lanes + b * 64 + h1, v);
-          if (c < p.l.d) {
+      if (whole) {
+        // two lanes swap a head each: a lane then stores two channels of one head
+        const int odd = lane & 1;
+        for (int b = 0; b < nblk; ++b) {
+          const int c = b * kBlock + 32 * warp + lane - odd;
+          __nv_bfloat16* to = p.O + (out + odd) * p.l.d + c;
+          for (int h1 = 0; h1 < heads; h1 += 16, to += 16 * p.l.d) {
+            uint32_t v[16] = {};
+            if (x.j1 > x.j0) tmem_ld_x16(tmem + lanes + b * 64 + h1, v);
+            uint32_t o[8];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int h = h1 + k;
-              if (h < heads) {
-                const float o = __uint_as_float(v[k]);
-                if (whole)
-                  p.O[(out + h) * p.l.d + c] = __float2bfloat16_rn(o * ctl->inv[h]);
-                else
-                  p.part[(slot * p.tile_heads + h) * p.l.d + c] = o;
-              }
+            for (int k = 0; k < 8; ++k) {
+              const float2 f = *reinterpret_cast<const float2*>(ctl->inv + h1 + 2 * k);
+              const float even_h = __uint_as_float(v[2 * k]) * f.x, odd_h = __uint_as_float(v[2 * k + 1]) * f.y;
+              const float give = odd ? even_h : odd_h, keep = odd ? odd_h : even_h;
+              const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+              o[k] = odd ? ptx::pack_bf16x2(got, keep) : ptx::pack_bf16x2(keep, got);
             }
+            if (c < p.l.d) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (h1 + 2 * k + odd < heads) *reinterpret_cast<uint32_t*>(to + 2 * k * p.l.d) = o[k];
+            }
+            __syncwarp();
           }
-          __syncwarp();
+        }
+      } else {
+        for (int b = 0; b < nblk; ++b) {
+          const int c = b * kBlock + 32 * warp + lane;
+          float* to = p.part + slot * p.tile_heads * p.l.d + c;
+          for (int h1 = 0; h1 < p.tile_heads; h1 += 16, to += 16 * p.l.d) {
+            uint32_t v[16];
+            tmem_ld_x16(tmem + lanes + b * 64 + h1, v);
+            if (c < p.l.d) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) to[k * p.l.d] = __uint_as_float(v[k]);
+            }
+            __syncwarp();
+          }
         }
       }
       ptx::tc_fence_before();  // the next row's products overwrite O^T after this thread's next weights
     }
     if (!begun && tid == 0 && p.split) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      const uint32_t id_s = ptx::idesc_bf16_f32(64, kTile, false, false);
-      const uint32_t id_o = ptx::idesc_bf16_f32(128, p.tile_heads, true, false);
-      uint32_t g = 0, item = 0, n = 0;  // tiles, pieces with tiles, stages filled so far
-      bool ok = true;
-      // O^T += C^T P^T of tile t, whose first stage is the n0-th
-      const auto weigh = [&](uint32_t t, uint32_t n0, bool first) {
-        if (!wait_bar(bar(ctl->p_full[t & 1]), (t >> 1) & 1, abort_flag, kFaultMma)) return false;
-        ptx::tc_fence_after();
-        const uint32_t pt = base + kOffP + (t & 1) * 8192u;
-        for (int b = 0; b < nblk; ++b) {
-          const uint32_t s = (n0 + b) % kStages, st = base + kOffRing + s * kStageBytes;
-          for (int k = 0; k < kTile / 16; ++k)
-            ptx::tc_mma_ss(tmem + b * 64, ptx::smem_desc_sw128(st + k * 2048, kHalf, 1024),
-                           ptx::smem_desc_sw128(pt + k * 32, 16, 1024), id_o, !first || k > 0);
-          ptx::tc_commit(bar(ctl->empty[s]));
-        }
-        ptx::tc_commit(bar(ctl->o_done[t & 1]));
-        return true;
-      };
-      while (ok && w.next(p, x)) {
-        if (x.j1 == x.j0) continue;
-        if (!wait_bar(bar(ctl->q_full), item & 1, abort_flag, kFaultMma)) break;
-        for (int j = x.j0; ok && j < x.j1; ++j) {
-          const uint32_t n0 = n;
-          for (int b = 0; ok && b < nblk; ++b, ++n) {
-            const uint32_t s = n % kStages, st = base + kOffRing + s * kStageBytes;
-            ok = wait_bar(bar(ctl->full[s]), (n / kStages) & 1, abort_flag, kFaultMma);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            const int steps = min(8, (p.l.d - b * kBlock + 15) / 16);
-            for (int k = 0; k < steps; ++k) {
-              const uint32_t at = (k >> 2) * 8192u + (k & 3) * 32u;
-              ptx::tc_mma_ss(tmem + kColS + (g & 1) * 64,
-                             ptx::smem_desc_sw128(base + kOffQ + b * 16384u + at, 16, 1024),
-                             ptx::smem_desc_sw128(st + at, 16, 1024), id_s, b > 0 || k > 0);
-            }
-          }
-          if (!ok) break;
-          ptx::tc_commit(bar(ctl->s_full[g & 1]));
-          if (j == x.j1 - 1) ptx::tc_commit(bar(ctl->q_empty));
-          // a tile's second product goes out behind the next tile's first, so
-          // that the softmax of one runs beside the products of the other
-          if (j > x.j0) ok = weigh(g - 1, n0 - nblk, j - 1 == x.j0);
-          if (ok && j == x.j1 - 1) ok = weigh(g, n0, j == x.j0);
-          ++g;
-        }
-        ++item;
-      }
-      // nothing may be in flight when the thread block frees TMEM
-      ptx::tc_commit(bar(ctl->drained));
-      wait_bar_noabort(bar(ctl->drained), 0);
-    }
-    __syncwarp();
-  } else if (warp == kQueryWarp) {
-    // ---------------------------------------------------------------- queries
-    if (lane == 0) {
-      const int chunks = (p.l.d + 63) / 64;
-      uint32_t item = 0;
-      while (w.next(p, x)) {
-        if (x.j1 == x.j0) continue;
-        if (item > 0 && !wait_bar(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultQuery)) break;
+  } else if (warp == kScoreWarp) {
+    // ---------------------------------------------------------------- queries, S
+    // The whole warp walks; an elected lane issues each batch of products from
+    // warp-uniform operands (a lone thread took 110-130 cycles an MMA to set
+    // them up, against 33 and 49 of the tensor core for S and O^T).
+    const uint32_t id_s = ptx::idesc_bf16_f32(64, kTile, false, false);
+    // operands' descriptors, to which address steps (in 16-byte units) are added
+    const uint64_t q_desc = ptx::smem_desc_sw128(base + kOffQ, 16, 1024);
+    const uint64_t c_desc = ptx::smem_desc_sw128(base + kOffRing, 16, 1024);
+    const int chunks = (p.l.d + 63) / 64;
+    const int tail = (p.l.d - (nblk - 1) * kBlock + 15) / 16;  // K steps in the last block
+    uint32_t g = 0, item = 0, s = 0, phase = 0;
+    while (w.next(p, x)) {
+      const int j0 = __shfl_sync(0xFFFFFFFFu, x.j0, 0), j1 = __shfl_sync(0xFFFFFFFFu, x.j1, 0);
+      if (j1 == j0) continue;
+      if (item > 0) wait_bar(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultScore);
+      if (ptx::elect_one()) {
         ptx::mbar_arrive_expect_tx(bar(ctl->q_full), chunks * p.tile_heads * 128);
         for (int c = 0; c < chunks; ++c)
-          ptx::tma_load_3d(base + kOffQ + c * 8192u, &p.tm_q, c * 64, x.head_tile * p.tile_heads, static_cast<int>(x.row),
-                      bar(ctl->q_full));
-        ++item;
+          ptx::tma_load_3d(base + kOffQ + c * 8192u, &p.tm_q, c * 64, x.head_tile * p.tile_heads,
+                           static_cast<int>(x.row), bar(ctl->q_full));
       }
-      if (item > 0) wait_bar_noabort(bar(ctl->q_full), (item - 1) & 1);
+      __syncwarp();
+      wait_bar(bar(ctl->q_full), item & 1, abort_flag, kFaultScore);
+      for (int j = j0; j < j1; ++j, ++g) {
+        if (g >= 2) wait_bar(bar(ctl->s_empty[g & 1]), ((g >> 1) - 1) & 1, abort_flag, kFaultScore);
+        const uint32_t ds = tmem + kColS + (g & 1) * 64;
+        for (int b = 0; b < nblk; ++b) {
+          wait_bar(bar(ctl->full[s]), phase, abort_flag, kFaultScore);
+          // The loading threads' stores become visible to the tensor core by a
+          // fence on this side of the barrier: on theirs it would wait for
+          // their loads in flight, a memory latency a block.
+          ptx::fence_proxy_async_smem();
+          ptx::tc_fence_after();
+          const uint64_t qd = q_desc + b * (16384u >> 4), cd = c_desc + s * (kStageBytes >> 4);
+          const bool last = b == nblk - 1;
+          if (ptx::elect_one()) {
+            ptx::tc_mma_ss(ds, qd, cd, id_s, b > 0);
+            const int steps = last ? tail : 8;
+#pragma unroll
+            for (int k = 1; k < 8; ++k) {
+              const uint32_t at = ((k >> 2) * 8192u + (k & 3) * 32u) >> 4;
+              if (k < steps) ptx::tc_mma_ss(ds, qd + at, cd + at, id_s, 1);
+            }
+            if (last) {
+              ptx::tc_commit(bar(ctl->s_full[g & 1]));
+              if (j == j1 - 1) ptx::tc_commit(bar(ctl->q_empty));
+            }
+          }
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      ++item;
     }
+    // nothing may be in flight when the thread block leaves
+    if (item > 0) wait_bar_noabort(bar(ctl->q_full), (item - 1) & 1);
+    if (ptx::elect_one()) ptx::tc_commit(bar(ctl->drained[0]));
     __syncwarp();
-  } else {
-    // ---------------------------------------------------------------- cache rows
-    const int lt = tid - 32 * kLoadWarp;
-    const int j = lt & 7, tok = lt >> 3;
-    // the tiles in order: (row, first token, tokens)
-    int64_t row = 0;
+    wait_bar_noabort(bar(ctl->drained[0]), 0);
+    __syncwarp();
+  } else if (warp == kValueWarp) {
+    // ---------------------------------------------------------------- O^T += C^T P^T
+    const uint32_t id_o = ptx::idesc_bf16_f32(128, p.tile_heads, true, false);
+    const uint64_t c_desc = ptx::smem_desc_sw128(base + kOffRing, kHalf, 1024);
+    const uint64_t p_desc = ptx::smem_desc_sw128(base + kOffP, 16, 1024);
+    uint32_t g = 0, s = 0;
+    while (w.next(p, x)) {
+      const int tiles = __shfl_sync(0xFFFFFFFFu, x.j1 - x.j0, 0);
+      for (int j = 0; j < tiles; ++j, ++g) {
+        wait_bar(bar(ctl->p_full[g & 1]), (g >> 1) & 1, abort_flag, kFaultValue);
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_after();
+        const uint64_t pd = p_desc + (g & 1) * (8192u >> 4);
+        for (int b = 0; b < nblk; ++b) {
+          const uint64_t cd = c_desc + s * (kStageBytes >> 4);
+          if (ptx::elect_one()) {
+            ptx::tc_mma_ss(tmem + b * 64, cd, pd, id_o, j > 0);
+#pragma unroll
+            for (int k = 1; k < kTile / 16; ++k)
+              ptx::tc_mma_ss(tmem + b * 64, cd + k * (2048 >> 4), pd + k * (32 >> 4), id_o, 1);
+            ptx::tc_commit(bar(ctl->empty[s]));
+            if (b == nblk - 1) ptx::tc_commit(bar(ctl->o_done[g & 1]));
+          }
+          __syncwarp();
+          if (++s == kStages) s = 0;
+        }
+      }
+    }
+    if (ptx::elect_one()) ptx::tc_commit(bar(ctl->drained[1]));
+    __syncwarp();
+    wait_bar_noabort(bar(ctl->drained[1]), 0);
+    __syncwarp();
+  } else if (warp == kTokenWarp) {
+    // ---------------------------------------------------------------- slots and masks
+    // A lane takes tokens lane and lane + 32 of each tile; table entries are
+    // loaded one tile ahead.
+    uint32_t g = 0;
     int tile = 0, end = 0, ntok = 0;
-    const auto next_slots = [&](int(&slot)[2]) {
+    Ref ref[2];
+    const auto look_up = [&]() {
       while (tile == end) {
         if (!w.next(p, x)) return false;
-        row = x.row;
         tile = x.j0;
         end = x.j1;
-        ntok = tokens_of(p, row);
+        ntok = tokens_of(p, x.row);
       }
+#pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int t = tile * kTile + tok + 32 * k;
-        slot[k] = t < ntok ? slot_of(p, row, t) : -1;
+        const int t = tile * kTile + lane + 32 * k;
+        ref[k] = t < ntok ? ref_of(p, x.row, t) : Ref{-1, 0};
       }
       ++tile;
       return true;
     };
-    const auto load_scales = [&](const int(&slot)[2], uint2(&sc)[2]) {
-      for (int k = 0; k < 2; ++k)
-        sc[k] = E4M3 && slot[k] >= 0
-                    ? __ldg(reinterpret_cast<const uint2*>(p.cache + static_cast<int64_t>(slot[k]) * p.l.row_bytes +
-                                                           p.l.scale_off))
-                    : make_uint2(0u, 0u);
-    };
-    Raw raw;
-    uint2 scales[2], scales1[2];
-    int slot[2], slot1[2] = {-1, -1};
-    bool live = next_slots(slot), live1 = false;
-    if (live) {
-      load_scales(slot, scales);
-#pragma unroll
-      for (int b = 0; b < kMaxBlocks; ++b)
-        if (b < nblk) load_block<E4M3>(p, raw, b, j, slot);
-      live1 = next_slots(slot1);
+    // behind the last tile, one mark for each loading warp to find
+    int marks = (load_warps - 1) / units + 1;
+    for (bool live = look_up(), ok = true; ok && (live || marks > 0); ++g) {
+      const int s0 = live ? slot_of(p, ref[0]) : kNoTile, s1 = live ? slot_of(p, ref[1]) : kNoTile;
+      const bool more = live && look_up();
+      const uint32_t i = g % kSlotRing;
+      if (g >= kSlotRing) ok = wait_bar(bar(ctl->slots_empty[i]), (g / kSlotRing - 1) & 1, abort_flag, kFaultToken);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      ctl->slot[i][lane] = s0;
+      ctl->slot[i][lane + 32] = s1;
+      const uint32_t lo = __ballot_sync(0xFFFFFFFFu, s0 >= 0), hi = __ballot_sync(0xFFFFFFFFu, s1 >= 0);
+      if (lane == 0 && live) ctl->mask[g % kMaskRing] = lo | static_cast<uint64_t>(hi) << 32;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_full[i]));
+      if (!live) --marks;
+      live = more;
     }
-    uint32_t n = 0, g = 0;
-    bool ok = true;
-    while (ok && live) {
-      int slot2[2] = {-1, -1};
-      const bool live2 = live1 && next_slots(slot2);
-      load_scales(slot1, scales1);
-      // masks: this warp's tokens are 4 * (warp - kLoadWarp) + 0..3, and those + 32
-      const uint32_t b0 = __ballot_sync(0xFFFFFFFFu, slot[0] >= 0), b1 = __ballot_sync(0xFFFFFFFFu, slot[1] >= 0);
-      if (lane == 0) {
-        const auto nibble = [](uint32_t v) {
-          return static_cast<unsigned char>((v & 1u) | (v >> 7 & 2u) | (v >> 14 & 4u) | (v >> 21 & 8u));
-        };
-        unsigned char* mk = reinterpret_cast<unsigned char*>(ctl->mask[g % kMaskRing]);
-        mk[warp - kLoadWarp] = nibble(b0);
-        mk[8 + warp - kLoadWarp] = nibble(b1);
+  } else {
+    // ---------------------------------------------------------------- cache rows
+    // units are counted over all tiles; this warp takes every load_warps-th
+    uint32_t n = warp - kLoadWarp;
+    for (bool ok = warp - kLoadWarp < load_warps; ok; n += load_warps) {
+      const uint32_t g = n / units, u = n - g * units, i = g % kSlotRing;
+      const int* slots = ctl->slot[i];
+      ok = wait_bar(bar(ctl->slots_full[i]), (g / kSlotRing) & 1, abort_flag, kFaultLoad);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      if (slots[0] == kNoTile) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_empty[i]));
+        break;
       }
-#pragma unroll
-      for (int b = 0; b < kMaxBlocks; ++b) {
-        if (b < nblk && ok) {
-          const uint32_t s = n % kStages;
-          if (lane == 0 && n >= kStages)
-            ok = wait_bar(bar(ctl->empty[s]), (n / kStages - 1) & 1, abort_flag, kFaultLoad);
-          ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-          if (ok) {
-            store_block<E4M3>(p, raw, b, j, tok, scales, base + kOffRing + s * kStageBytes);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(ctl->full[s]));
-            if (live1) load_block<E4M3>(p, raw, b, j, slot1);
-            ++n;
-          }
-        }
+      UnitShape q = {};
+      RawUnit raw;
+      if (E4M3) {
+        q = unit_shape(p.l, nblk, u, lane);
+        load_unit(p, raw, q, slots, lane);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_empty[i]));
       }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        slot[k] = slot1[k];
-        slot1[k] = slot2[k];
-        scales[k] = scales1[k];
+      const uint32_t block = g * nblk + (E4M3 ? q.b : u), s = block % kStages;
+      const uint32_t stage = base + kOffRing + s * kStageBytes;
+      // the phase of `empty` that lets the stage be filled (the one before the first counts as done)
+      ok = wait_bar(bar(ctl->empty[s]), (block / kStages + 1) & 1, abort_flag, kFaultLoad);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      if (E4M3) {
+        store_unit(p.l, raw, q, lane, stage);
+        ptx::mbar_arrive_n(bar(ctl->full[s]), q.wide ? 1 : 2);
+      } else {
+        copy_block(p, slots, u, lane, stage);
+        copies_arrive(bar(ctl->full[s]));
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_empty[i]));
       }
-      live = live1;
-      live1 = live2;
-      ++g;
     }
+    if (!E4M3) asm volatile("cp.async.wait_all;" ::: "memory");  // nothing lands after the block has left
   }
 
   // ------------------------------------------------------------------ teardown
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
@@ -945,7 +1102,7 @@ int attend(AttnParams& p, const void* q, void* workspace, size_t workspace_bytes
 }
 
 AttnParams params(const RowLayout& l, const void* cache, const int32_t* table, const int32_t* lens, void* O, float* lse,
-                  int64_t rows, int64_t width, int64_t num_pages, int page_size, int nh, double scale) {
+                  int64_t rows, int64_t width, int num_pages, int page_size, int nh, double scale) {
   AttnParams p = {};
   p.cache = static_cast<const char*>(cache);
   p.table = table;
@@ -954,7 +1111,7 @@ AttnParams params(const RowLayout& l, const void* cache, const int32_t* table, c
   p.lse = lse;
   p.rows = rows;
   p.width = width;
-  p.num_slots = num_pages * page_size;
+  p.num_slots = static_cast<int64_t>(num_pages) * page_size;
   p.num_pages = num_pages;
   p.nh = nh;
   p.page_size = page_size;
@@ -998,7 +1155,8 @@ extern "C" int latent_attn_decode(const void* q, const void* cache, const int32_
   if (num_pages > 0x7FFFFFFF / page_size || max_pages > 0x7FFFFFFF / page_size) return INVROPE_ERR_UNSUPPORTED;
   if ((st = check_shape(rows, nh, max_pages * page_size, scale)) != INVROPE_OK) return st;
   if (rows > 0 && !lens) return INVROPE_ERR_INVALID_ARG;
-  AttnParams p = params(l, cache, page_table, lens, O, lse, rows, max_pages, num_pages, page_size, nh, scale);
+  AttnParams p = params(l, cache, page_table, lens, O, lse, rows, max_pages, static_cast<int>(num_pages), page_size, nh,
+                        scale);
   return attend(p, q, workspace, workspace_bytes, fmt, max_pages * page_size, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -1011,6 +1169,6 @@ extern "C" int latent_attn_sparse(const void* q, const void* cache, const int32_
   if (num_slots < 1 || topk < 0) return INVROPE_ERR_INVALID_ARG;
   if (num_slots > 0x7FFFFFFF) return INVROPE_ERR_UNSUPPORTED;
   if ((st = check_shape(rows, nh, topk, scale)) != INVROPE_OK) return st;
-  AttnParams p = params(l, cache, idx, nullptr, O, lse, rows, topk, num_slots, 1, nh, scale);
+  AttnParams p = params(l, cache, idx, nullptr, O, lse, rows, topk, static_cast<int>(num_slots), 1, nh, scale);
   return attend(p, q, workspace, workspace_bytes, fmt, topk, reinterpret_cast<cudaStream_t>(stream));
 }
