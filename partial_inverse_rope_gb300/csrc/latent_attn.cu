@@ -57,11 +57,11 @@ constexpr int kMinUnits = 4;     // units of the line a thread block takes at le
 
 constexpr int kSoftmaxThreads = 128;
 constexpr int kScoreWarp = 4, kValueWarp = 5, kTokenWarp = 6, kLoadWarp = 7;
-// Loading warps take blocks in turn. At most kStages and, over all blocks of a
-// tile, kSlotRing tiles apart: a parity then tells the phase a warp waits for
-// from the one before the one before.
-constexpr int kLoadWarps = kStages;
-constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+template <bool E4M3>
+constexpr int kLoadWarps = E4M3 ? 16 : 8;
+template <bool E4M3>
+constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps<E4M3>);
+constexpr int kMaxWarps = kLoadWarp + 16;
 
 // shared memory, from a 1024-byte boundary
 constexpr int kOffQ = 0;                                    // 8 x [64 heads][64 channels]
@@ -76,7 +76,7 @@ struct Ctl {
   int slot[kSlotRing][kTile];   // -1: left out; kNoTile: no more tiles
   float factor[2][64];
   float inv[64];
-  int64_t sums[kThreads / 32];
+  int64_t sums[kMaxWarps];
   int64_t base;
   int row;
   int abort;
@@ -210,6 +210,7 @@ struct Walk {
 
 // Runs of the line: the whole line's units and this block's first row. All
 // threads of the block call it.
+template <int kThreads>
 __device__ void find_run(const AttnParams& p, Ctl* ctl, Walk* w, int64_t* total, int64_t* nrun) {
   const int tid = threadIdx.x;
   if (!p.lens) {  // every row is as long: no table of lengths to add up
@@ -262,14 +263,6 @@ __device__ void find_run(const AttnParams& p, Ctl* ctl, Walk* w, int64_t* total,
   if (static_cast<int64_t>(blockIdx.x) >= *nrun) w->hi = w->at = 0;  // nothing to do
 }
 
-__device__ __forceinline__ uint4 load_16(const char* at) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(at));
-  return v;
-}
-
 __device__ __forceinline__ void store_16(uint32_t at, const uint4& v) { ptx::st_shared_v4(at, v.x, v.y, v.z, v.w); }
 
 __device__ __forceinline__ uint32_t unit_addr(uint32_t stage, int tok, int unit) {  // 8 channels a unit
@@ -308,107 +301,138 @@ __device__ __forceinline__ void copy_block(const AttnParams& p, const int* slots
   }
 }
 
-// A warp's share of an e4m3 tile, held in its registers while in flight. Of a
-// block of codes only, the whole block: 8 lanes take a token (16 codes each), 4
-// tokens a step, 16 steps. Of a block with pe channels, 32 tokens: 16 lanes take
-// a token, those past its codes one unit of 8 bf16 values each, 2 tokens a step.
-struct RawUnit {
-  uint4 v[16];
-  uint32_t scales;  // the block's two scale bytes of tokens lane (low half) and lane + 32
-};
+// Loading warps' shares ("units") of an e4m3 tile: of each channel block its
+// codes, held in the warp's registers while in flight and converted then (a
+// block with more than 4 items of 16 codes a token: its tokens' first and second
+// half apart), and its pe channels, copied as they are.
 struct UnitShape {
-  int b, codes, units;  // channel block, and its 16-code items and 8-value pe units of a token
-  bool wide;            // with pe channels
-  int first, step;      // this lane's tokens
-  int item;             // and its item of each
+  int b;       // channel block
+  int codes;   // items of 16 codes that the block has of a token
+  bool pe;     // this unit: the block's pe channels
+  int lanes;   // code units: lanes a token (a power of two >= codes), 32 / lanes tokens a step
+  int token;   // code units: the first token
+  int weight;  // arrivals of a lane on the stage's barrier, kArrivals over the block's units
 };
-// Units of a tile: the blocks in order, those with pe channels as two.
-__device__ __forceinline__ int units_of(const RowLayout& l, int nblk) {
-  return l.pe > 0 ? 2 * nblk - l.nope / kBlock : nblk;
+constexpr int kArrivals = 6;
+__device__ __forceinline__ int codes_of(const RowLayout& l, int b) {
+  return min(max(l.nope - b * kBlock, 0), kBlock) / 16;
 }
-__device__ __forceinline__ UnitShape unit_shape(const RowLayout& l, int nblk, int u, int lane) {
-  const int plain = l.pe > 0 ? l.nope / kBlock : nblk;
+__device__ __forceinline__ int units_of(const RowLayout& l, int b) {
+  const int codes = codes_of(l, b);
+  return (codes > 4 ? 2 : codes > 0 ? 1 : 0) + (min(l.d, (b + 1) * kBlock) > l.nope ? 1 : 0);
+}
+__device__ __forceinline__ UnitShape unit_shape(const RowLayout& l, int u) {
+  int b = 0, n = units_of(l, 0);
+  while (u >= n) {
+    u -= n;
+    n = units_of(l, ++b);
+  }
   UnitShape q;
-  q.wide = u >= plain;
-  q.b = q.wide ? plain + (u - plain) / 2 : u;
-  const int c0 = q.b * kBlock;
-  q.codes = min(max(l.nope - c0, 0), kBlock) / 16;
-  q.units = q.wide ? max(min(l.d, c0 + kBlock) - max(l.nope, c0), 0) / 8 : 0;
-  q.item = q.wide ? lane & 15 : lane & 7;
-  q.step = q.wide ? 2 : 4;
-  q.first = q.wide ? 32 * ((u - plain) & 1) + (lane >> 4) : lane >> 3;
+  q.b = b;
+  q.codes = codes_of(l, b);
+  q.lanes = q.codes > 4 ? 8 : q.codes > 2 ? 4 : q.codes;
+  const int halves = q.codes > 4 ? 2 : q.codes > 0 ? 1 : 0;
+  q.pe = u >= halves;
+  q.token = 32 * u;
+  q.weight = kArrivals / n;
   return q;
 }
 
-__device__ __forceinline__ void load_unit(const AttnParams& p, RawUnit& raw, const UnitShape& q, const int* slots,
-                                          int lane) {
-  const int c0 = q.b * kBlock;
-  // byte offset in the row of this lane's item
-  const int at = q.item < q.codes ? c0 + 16 * q.item
-                                  : p.l.nope + 2 * max(c0 - p.l.nope, 0) + 16 * (q.item - q.codes);
-  const bool mine = q.item < q.codes + q.units;
+// The codes of a unit: of token `token` + lane / lanes + (32 / lanes) k in step
+// k the 16 codes lane % lanes; 8 steps of half a block's tokens, or fewer of all.
+struct RawCodes {
+  uint4 v[8];
+  uint32_t scales;  // the block's two scale bytes of tokens `token` + lane (low half) and + 32
+};
+
+__device__ __forceinline__ void load_16_if(uint4& v, const char* at, bool there) {  // 0 where it is not
+  v = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "l"(at), "r"(static_cast<int>(there)));
+}
+
+template <int L>
+constexpr int kSteps = L == 8 ? 8 : 2 * L;
+
+template <int L>
+__device__ __forceinline__ void load_codes(const AttnParams& p, RawCodes& raw, const UnitShape& q, const int* slots,
+                                           int lane) {
+  const int item = lane % L, first = q.token + lane / L;
+  const char* from = p.cache + q.b * kBlock + 16 * item;
+  int slot[kSteps<L>];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int slot = slots[q.first + q.step * k];
-    raw.v[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (mine && slot >= 0) raw.v[k] = load_16(p.cache + static_cast<int64_t>(slot) * p.l.row_bytes + at);
-  }
+  for (int k = 0; k < kSteps<L>; ++k) slot[k] = slots[first + (32 / L) * k];
+#pragma unroll
+  for (int k = 0; k < kSteps<L>; ++k)
+    load_16_if(raw.v[k], from + static_cast<int64_t>(slot[k]) * p.l.row_bytes, slot[k] >= 0 && item < q.codes);
   unsigned short two[2] = {0, 0};
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int slot = slots[lane + 32 * k];
-    if (slot >= 0 && q.codes > 0)  // rows end on a 16-byte boundary: two bytes are there even where one group is
+  for (int k = 0; k < (L == 8 ? 1 : 2); ++k) {
+    const int s = slots[q.token + lane + 32 * k];
+    if (s >= 0)  // rows end on a 16-byte boundary: two bytes are there even where one group is
       asm volatile("ld.global.nc.u16 %0, [%1];"
                    : "=h"(two[k])
-                   : "l"(p.cache + static_cast<int64_t>(slot) * p.l.row_bytes + p.l.scale_off + 2 * q.b));
+                   : "l"(p.cache + static_cast<int64_t>(s) * p.l.row_bytes + p.l.scale_off + 2 * q.b));
   }
   raw.scales = two[0] | static_cast<uint32_t>(two[1]) << 16;
 }
 
-__device__ __forceinline__ void store_unit(const RowLayout& l, const RawUnit& raw, const UnitShape& q, int lane,
-                                           uint32_t stage) {
-  // 2^(byte - 127) times the 2^120 of the conversion, as one bf16 factor; a
-  // scale of more than 2^7 has no such product and takes two.
-  uint32_t byte[16];
-  bool large = false;
+template <int L>
+__device__ __forceinline__ void store_codes(const RawCodes& raw, const UnitShape& q, int lane, uint32_t stage) {
+  const int item = lane % L, first = lane / L;
+  const int odd = item >> 2;  // also the item's scale of the two
+  // 2^(byte - 127) times the 2^120 of the conversion is one bf16 factor up to a
+  // scale of 2^7; above, 2^127 is, and the rest of it another.
+  const auto over = [](uint32_t byte) { return byte > 134u && byte != 255u; };
+  const uint32_t s4 = raw.scales;
+  const bool large = __any_sync(0xFFFFFFFFu, over(s4 & 255u) || over(s4 >> 8 & 255u) || over(s4 >> 16 & 255u) ||
+                                                over(s4 >> 24));
+  const uint32_t row = stage + q.token * 128;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int t = q.first + q.step * k;
-    const uint32_t two = __shfl_sync(0xFFFFFFFFu, raw.scales, t & 31) >> (16 * (t >> 5));
-    byte[k] = (two >> (8 * ((q.item >> 2) & 1))) & 255u;
-    large = large || (byte[k] > 134u && byte[k] != 255u);
-  }
-  large = __any_sync(0xFFFFFFFFu, large && q.item < q.codes);
-  // the first unit of 8 channels in the block that pe lanes write
-  const int pe_unit = max(l.nope - q.b * kBlock, 0) / 8 + q.item - q.codes;
-  const int odd = (q.item >> 2) & 1;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int t = q.first + q.step * k;
-    if (q.item < q.codes) {
-      const uint4 w = raw.v[k];
-      uint4 lo, hi;
-      if (!large) {
-        const uint32_t f = byte[k] == 255u ? 0x7FC0u : (byte[k] + 120u) << 7;
-        const uint32_t f2 = f | f << 16;
-        latent::e4m3x4_times(w.x, f2, lo.x, lo.y);
-        latent::e4m3x4_times(w.y, f2, lo.z, lo.w);
-        latent::e4m3x4_times(w.z, f2, hi.x, hi.y);
-        latent::e4m3x4_times(w.w, f2, hi.z, hi.w);
-      } else {
-        const uint32_t f2 = latent::scale_bf16x2(byte[k]);
-        latent::e4m3x4_to_bf16(w.x, f2, lo.x, lo.y);
-        latent::e4m3x4_to_bf16(w.y, f2, lo.z, lo.w);
-        latent::e4m3x4_to_bf16(w.z, f2, hi.x, hi.y);
-        latent::e4m3x4_to_bf16(w.w, f2, hi.z, hi.w);
-      }
-      // lanes of the two 64-channel halves write the even and the odd unit
-      // first in turn: 8 lanes of a token then cover all 32 banks
-      store_16(unit_addr(stage, t, 2 * q.item + odd), odd ? hi : lo);
-      store_16(unit_addr(stage, t, 2 * q.item + 1 - odd), odd ? lo : hi);
-    } else if (pe_unit < 16) {  // a pe unit, or zeros behind the last channel
-      store_16(unit_addr(stage, t, pe_unit), raw.v[k]);
+  for (int k = 0; k < kSteps<L>; ++k) {
+    const int t = first + (32 / L) * k;
+    const uint32_t two = __shfl_sync(0xFFFFFFFFu, s4, t & 31) >> (k < L ? 0 : 16);
+    const uint32_t byte = (two >> (8 * odd)) & 255u;
+    uint32_t f = byte == 255u ? 0x7FC0u : min(byte + 120u, 254u) << 7;
+    f |= f << 16;
+    const uint4 w = raw.v[k];
+    uint4 lo, hi;
+    latent::e4m3x4_times(w.x, f, lo.x, lo.y);
+    latent::e4m3x4_times(w.y, f, lo.z, lo.w);
+    latent::e4m3x4_times(w.z, f, hi.x, hi.y);
+    latent::e4m3x4_times(w.w, f, hi.z, hi.w);
+    if (large) {
+      const uint32_t r = latent::scale_bf16x2(over(byte) ? byte - 7u : 127u);
+      lo.x = latent::mul_bf16x2(lo.x, r), lo.y = latent::mul_bf16x2(lo.y, r);
+      lo.z = latent::mul_bf16x2(lo.z, r), lo.w = latent::mul_bf16x2(lo.w, r);
+      hi.x = latent::mul_bf16x2(hi.x, r), hi.y = latent::mul_bf16x2(hi.y, r);
+      hi.z = latent::mul_bf16x2(hi.z, r), hi.w = latent::mul_bf16x2(hi.w, r);
     }
+    if (item < q.codes) {
+      // lanes of the two 64-channel halves write the even and the odd unit
+      // first in turn: the lanes of a token then cover all 32 banks
+      store_16(unit_addr(row, t, 2 * item + odd), odd ? hi : lo);
+      store_16(unit_addr(row, t, 2 * item + 1 - odd), odd ? lo : hi);
+    }
+  }
+}
+
+// The pe channels of a block, and zeros behind the last channel: 16 lanes take
+// a token's units of 8 channels.
+__device__ __forceinline__ void copy_pe(const AttnParams& p, const UnitShape& q, const int* slots, int lane,
+                                        uint32_t stage) {
+  const int unit = lane & 15, half = lane >> 4, c = q.b * kBlock + 8 * unit;
+  const bool mine = c >= p.l.nope, there = mine && c < p.l.d;
+  const char* from = p.cache + (there ? p.l.nope + 2 * (c - p.l.nope) : 0);
+#pragma unroll 8
+  for (int k = 0; k < 32; ++k) {
+    const int t = 32 * half + k, slot = slots[t];
+    const bool ok = there && slot >= 0;
+    if (mine) copy_16(unit_addr(stage, t, unit), from + static_cast<int64_t>(ok ? slot : 0) * p.l.row_bytes, ok);
   }
 }
 
@@ -418,19 +442,23 @@ __device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp
   return r;
 }
 
+// (These loads end with their own wait: a register moved or spilled between a
+// load and a wait apart from it would be read too early.)
 // 16 lanes x 64 columns of fp32: thread t holds rows t / 4 (r[4j], r[4j+1]) and
 // t / 4 + 8 (r[4j+2], r[4j+3]) at columns 8 j + 2 (t % 4) and the next.
 __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
         "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+      : "r"(taddr)
+      : "memory");
 }
 
 // 16 columns of this thread's lane.
@@ -470,7 +498,7 @@ __device__ __forceinline__ bool any_softmax(bool x) {
 }
 
 template <bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(1024) char smem[];
   const uint32_t base = ptx::smem_u32(smem);
   if (base & 1023u) {  // never: the declaration asks for it
@@ -481,13 +509,20 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   volatile int* abort_flag = &ctl->abort;
   const int nblk = (p.l.d + kBlock - 1) / kBlock;
-  const int units = E4M3 ? units_of(p.l, nblk) : nblk;  // loading warps' shares of a tile
-  const int load_warps = min(kLoadWarps, kSlotRing * units);
+  int units = nblk;  // loading warps' shares of a tile
+  if (E4M3) {
+    units = 0;
+    for (int b = 0; b < nblk; ++b) units += units_of(p.l, b);
+  }
+  // Loading warps take units in turn; a warp's next is at most kStages blocks and
+  // kSlotRing tiles on (kStages - 1 on average is at most one less), so that a
+  // parity tells the phase it waits for from the one two before.
+  const int load_warps = min(min(kLoadWarps<E4M3>, kSlotRing * units), (kStages - 1) * units / nblk);
   const auto bar = [](uint64_t& b) { return ptx::smem_u32(&b); };
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(bar(ctl->full[s]), E4M3 ? 64 : 32);
+      ptx::mbar_init(bar(ctl->full[s]), E4M3 ? 32 * kArrivals : 32);
       ptx::mbar_init(bar(ctl->empty[s]), 1);
     }
     for (int i = 0; i < kSlotRing; ++i) {
@@ -512,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   }
   Walk w;
   int64_t total, nrun;
-  find_run(p, ctl, &w, &total, &nrun);
+  find_run<kThreads<E4M3>>(p, ctl, &w, &total, &nrun);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -539,7 +574,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
         uint32_t r[32];
         tmem_ld_16x64(tmem + kColS + (g & 1) * 64 + lanes, r);
         const uint64_t mask = ctl->mask[g % kMaskRing];
-        ptx::tmem_ld_wait(r);
         ptx::tc_fence_before();
         ptx::mbar_arrive(bar(ctl->s_empty[g & 1]));
         float s[32];
@@ -843,31 +877,47 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
         if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_empty[i]));
         break;
       }
-      UnitShape q = {};
-      RawUnit raw;
-      if (E4M3) {
-        q = unit_shape(p.l, nblk, u, lane);
-        load_unit(p, raw, q, slots, lane);
+      const UnitShape q = E4M3 ? unit_shape(p.l, u) : UnitShape{static_cast<int>(u), 0, true, 0, 0, 1};
+      RawCodes raw;
+      if (E4M3 && !q.pe) {
+        if (q.lanes == 8)
+          load_codes<8>(p, raw, q, slots, lane);
+        else if (q.lanes == 4)
+          load_codes<4>(p, raw, q, slots, lane);
+        else if (q.lanes == 2)
+          load_codes<2>(p, raw, q, slots, lane);
+        else
+          load_codes<1>(p, raw, q, slots, lane);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_empty[i]));
       }
-      const uint32_t block = g * nblk + (E4M3 ? q.b : u), s = block % kStages;
+      const uint32_t block = g * nblk + q.b, s = block % kStages;
       const uint32_t stage = base + kOffRing + s * kStageBytes;
       // the phase of `empty` that lets the stage be filled (the one before the first counts as done)
       ok = wait_bar(bar(ctl->empty[s]), (block / kStages + 1) & 1, abort_flag, kFaultLoad);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
-      if (E4M3) {
-        store_unit(p.l, raw, q, lane, stage);
-        ptx::mbar_arrive_n(bar(ctl->full[s]), q.wide ? 1 : 2);
+      if (E4M3 && !q.pe) {
+        if (q.lanes == 8)
+          store_codes<8>(raw, q, lane, stage);
+        else if (q.lanes == 4)
+          store_codes<4>(raw, q, lane, stage);
+        else if (q.lanes == 2)
+          store_codes<2>(raw, q, lane, stage);
+        else
+          store_codes<1>(raw, q, lane, stage);
+        ptx::mbar_arrive_n(bar(ctl->full[s]), q.weight);
       } else {
-        copy_block(p, slots, u, lane, stage);
-        copies_arrive(bar(ctl->full[s]));
+        if (E4M3)
+          copy_pe(p, q, slots, lane, stage);
+        else
+          copy_block(p, slots, q.b, lane, stage);
+        for (int k = 0; k < q.weight; ++k) copies_arrive(bar(ctl->full[s]));
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_empty[i]));
       }
     }
-    if (!E4M3) asm volatile("cp.async.wait_all;" ::: "memory");  // nothing lands after the block has left
+    asm volatile("cp.async.wait_all;" ::: "memory");  // nothing lands after the block has left
   }
 
   // ------------------------------------------------------------------ teardown
@@ -1080,9 +1130,9 @@ int attend(AttnParams& p, const void* q, void* workspace, size_t workspace_bytes
   p.tile_heads = n.tile_heads;
   if (!opt_in_smem(dev.device) || !query_map(&p.tm_q, q, p.rows, p.nh, p.l.d, n.tile_heads)) return INVROPE_ERR_CUDA;
   if (fmt == KV_LATENT_E4M3)
-    latent_attn_kernel<true><<<n.grid, kThreads, kSmem, s>>>(p);
+    latent_attn_kernel<true><<<n.grid, kThreads<true>, kSmem, s>>>(p);
   else
-    latent_attn_kernel<false><<<n.grid, kThreads, kSmem, s>>>(p);
+    latent_attn_kernel<false><<<n.grid, kThreads<false>, kSmem, s>>>(p);
   if ((st = check_launch()) != INVROPE_OK || n.bytes == 0) return st;
   // programmatic dependent launch: the join's launch is processed while the
   // attention drains; its blocks wait in-kernel for the partials
