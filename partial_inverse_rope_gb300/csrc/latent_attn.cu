@@ -119,8 +119,9 @@ struct AttnParams {
   RowLayout l;
 };
 
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned code) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
+// Out of line, like every path that is not taken often: the roles' code together
+// has to stay in the instruction cache.
+__device__ __noinline__ bool wait_bar_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned code) {
   const uint64_t t0 = ptx::globaltimer_ns();
   for (uint32_t n = 1;; ++n) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
@@ -132,10 +133,13 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
   }
 }
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned code) {
+  return ptx::mbar_try_wait(bar, parity) || wait_bar_on(bar, parity, abort_flag, code);
+}
 
 // Bounded wait that ignores the abort flag: for what must land before the
 // thread block frees what it is written to.
-__device__ __forceinline__ void wait_bar_noabort(uint32_t bar, uint32_t parity) {
+__device__ __noinline__ void wait_bar_noabort(uint32_t bar, uint32_t parity) {
   if (ptx::mbar_try_wait(bar, parity)) return;
   const uint64_t t0 = ptx::globaltimer_ns();
   while (!ptx::mbar_try_wait(bar, parity))
@@ -174,8 +178,8 @@ __device__ __forceinline__ int slot_of(const AttnParams& p, const Ref& x) {
 
 // First unit of thread block c's run of a line of `total` units cut into n runs,
 // and the run that unit x lies in.
-__device__ __forceinline__ int64_t run_begin(int64_t c, int64_t total, int64_t n) { return c * total / n; }
-__device__ __forceinline__ int64_t run_of(int64_t x, int64_t total, int64_t n) { return ((x + 1) * n - 1) / total; }
+__device__ __noinline__ int64_t run_begin(int64_t c, int64_t total, int64_t n) { return c * total / n; }
+__device__ __noinline__ int64_t run_of(int64_t x, int64_t total, int64_t n) { return ((x + 1) * n - 1) / total; }
 
 // This thread block's pieces of rows, in order. Every role walks them alike.
 struct Piece {
@@ -309,7 +313,7 @@ struct UnitShape {
   int b;       // channel block
   int codes;   // items of 16 codes that the block has of a token
   bool pe;     // this unit: the block's pe channels
-  int lanes;   // code units: lanes a token (a power of two >= codes), 32 / lanes tokens a step
+  int lanes;   // code units: lanes a token, 8 or 4
   int token;   // code units: the first token
   int weight;  // arrivals of a lane on the stage's barrier, kArrivals over the block's units
 };
@@ -330,7 +334,7 @@ __device__ __forceinline__ UnitShape unit_shape(const RowLayout& l, int u) {
   UnitShape q;
   q.b = b;
   q.codes = codes_of(l, b);
-  q.lanes = q.codes > 4 ? 8 : q.codes > 2 ? 4 : q.codes;
+  q.lanes = q.codes > 4 ? 8 : 4;
   const int halves = q.codes > 4 ? 2 : q.codes > 0 ? 1 : 0;
   q.pe = u >= halves;
   q.token = 32 * u;
@@ -339,7 +343,8 @@ __device__ __forceinline__ UnitShape unit_shape(const RowLayout& l, int u) {
 }
 
 // The codes of a unit: of token `token` + lane / lanes + (32 / lanes) k in step
-// k the 16 codes lane % lanes; 8 steps of half a block's tokens, or fewer of all.
+// k the 16 codes lane % lanes, so 8 steps take half a block's tokens, or all with
+// 4 lanes each.
 struct RawCodes {
   uint4 v[8];
   uint32_t scales;  // the block's two scale bytes of tokens `token` + lane (low half) and + 32
@@ -355,24 +360,21 @@ __device__ __forceinline__ void load_16_if(uint4& v, const char* at, bool there)
       : "l"(at), "r"(static_cast<int>(there)));
 }
 
-template <int L>
-constexpr int kSteps = L == 8 ? 8 : 2 * L;
-
-template <int L>
 __device__ __forceinline__ void load_codes(const AttnParams& p, RawCodes& raw, const UnitShape& q, const int* slots,
                                            int lane) {
-  const int item = lane % L, first = q.token + lane / L;
+  const int item = lane & (q.lanes - 1), first = q.token + (q.lanes == 8 ? lane >> 3 : lane >> 2);
+  const int step = q.lanes == 8 ? 4 : 8;
   const char* from = p.cache + q.b * kBlock + 16 * item;
-  int slot[kSteps<L>];
+  int slot[8];
 #pragma unroll
-  for (int k = 0; k < kSteps<L>; ++k) slot[k] = slots[first + (32 / L) * k];
+  for (int k = 0; k < 8; ++k) slot[k] = slots[first + step * k];
 #pragma unroll
-  for (int k = 0; k < kSteps<L>; ++k)
+  for (int k = 0; k < 8; ++k)
     load_16_if(raw.v[k], from + static_cast<int64_t>(slot[k]) * p.l.row_bytes, slot[k] >= 0 && item < q.codes);
   unsigned short two[2] = {0, 0};
 #pragma unroll
-  for (int k = 0; k < (L == 8 ? 1 : 2); ++k) {
-    const int s = slots[q.token + lane + 32 * k];
+  for (int k = 0; k < 2; ++k) {
+    const int s = k == 0 || q.lanes == 4 ? slots[q.token + lane + 32 * k] : -1;
     if (s >= 0)  // rows end on a 16-byte boundary: two bytes are there even where one group is
       asm volatile("ld.global.nc.u16 %0, [%1];"
                    : "=h"(two[k])
@@ -381,9 +383,9 @@ __device__ __forceinline__ void load_codes(const AttnParams& p, RawCodes& raw, c
   raw.scales = two[0] | static_cast<uint32_t>(two[1]) << 16;
 }
 
-template <int L>
 __device__ __forceinline__ void store_codes(const RawCodes& raw, const UnitShape& q, int lane, uint32_t stage) {
-  const int item = lane % L, first = lane / L;
+  const int item = lane & (q.lanes - 1), first = q.lanes == 8 ? lane >> 3 : lane >> 2;
+  const int step = q.lanes == 8 ? 4 : 8;
   const int odd = item >> 2;  // also the item's scale of the two
   // 2^(byte - 127) times the 2^120 of the conversion is one bf16 factor up to a
   // scale of 2^7; above, 2^127 is, and the rest of it another.
@@ -393,9 +395,9 @@ __device__ __forceinline__ void store_codes(const RawCodes& raw, const UnitShape
                                                 over(s4 >> 24));
   const uint32_t row = stage + q.token * 128;
 #pragma unroll
-  for (int k = 0; k < kSteps<L>; ++k) {
-    const int t = first + (32 / L) * k;
-    const uint32_t two = __shfl_sync(0xFFFFFFFFu, s4, t & 31) >> (k < L ? 0 : 16);
+  for (int k = 0; k < 8; ++k) {
+    const int t = first + step * k;
+    const uint32_t two = __shfl_sync(0xFFFFFFFFu, s4, t & 31) >> (16 * (t >> 5));
     const uint32_t byte = (two >> (8 * odd)) & 255u;
     uint32_t f = byte == 255u ? 0x7FC0u : min(byte + 120u, 254u) << 7;
     f |= f << 16;
@@ -880,14 +882,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       const UnitShape q = E4M3 ? unit_shape(p.l, u) : UnitShape{static_cast<int>(u), 0, true, 0, 0, 1};
       RawCodes raw;
       if (E4M3 && !q.pe) {
-        if (q.lanes == 8)
-          load_codes<8>(p, raw, q, slots, lane);
-        else if (q.lanes == 4)
-          load_codes<4>(p, raw, q, slots, lane);
-        else if (q.lanes == 2)
-          load_codes<2>(p, raw, q, slots, lane);
-        else
-          load_codes<1>(p, raw, q, slots, lane);
+        load_codes(p, raw, q, slots, lane);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_empty[i]));
       }
@@ -898,14 +893,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       if (E4M3 && !q.pe) {
-        if (q.lanes == 8)
-          store_codes<8>(raw, q, lane, stage);
-        else if (q.lanes == 4)
-          store_codes<4>(raw, q, lane, stage);
-        else if (q.lanes == 2)
-          store_codes<2>(raw, q, lane, stage);
-        else
-          store_codes<1>(raw, q, lane, stage);
+        store_codes(raw, q, lane, stage);
         ptx::mbar_arrive_n(bar(ctl->full[s]), q.weight);
       } else {
         if (E4M3)
