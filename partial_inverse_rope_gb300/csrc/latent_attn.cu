@@ -47,6 +47,7 @@ using latent::RowLayout;
 
 constexpr int kTile = 64;        // tokens per tile
 constexpr int kBlock = 128;      // channels per stage of the ring
+constexpr int kMaxBlocks = latent::kMaxD / kBlock;
 constexpr int kStages = 9;       // two tiles of 512 channels and one stage more
 constexpr int kStageBytes = kTile * kBlock * 2;
 constexpr int kHalf = kTile * 128;       // one 64-channel half of a stage
@@ -283,71 +284,32 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Block b of a bf16 tile: a warp's instruction covers 256 bytes of tokens k and
-// 32 + k.
-__device__ __forceinline__ void copy_block(const AttnParams& p, const int* slots, int b, int lane, uint32_t stage) {
-  const int unit = lane & 15, half = lane >> 4, c = b * kBlock + 8 * unit;
-  const bool mine = c < p.l.d;
-  const char* from = p.cache + (mine ? 2 * c : 0);
-  const uint32_t to = stage + (unit >> 3) * kHalf + half * 4096u;
-  const int4* s4 = reinterpret_cast<const int4*>(slots + 32 * half);
+// Every loading warp takes a few tokens of every block, so that a stage that
+// comes free is full again after the work of those few: with a block to a warp
+// its 32 copies, or 8 to 16 conversions, lay between any stage's release and
+// its next use (1100 and 2800-3500 cycles of a 6500-cycle loop).
+
+// bf16 rows: 8 tokens a warp, two an instruction (16 lanes a token's 256 bytes).
+__device__ __forceinline__ void copy_block(const AttnParams& p, const int (&slot)[4], int b, int tok, int lane,
+                                           uint32_t stage) {
+  const int unit = lane & 15, c = b * kBlock + 8 * unit;
+  const char* from = p.cache + (c < p.l.d ? 2 * c : 0);
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int4 s = s4[q];
-    const int slot[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = 4 * q + i;
-      const bool there = mine && slot[i] >= 0;
-      copy_16(to + k * 128u + (((unit & 7) ^ (k & 7)) << 4),
-              from + static_cast<int64_t>(there ? slot[i] : 0) * p.l.row_bytes, there);
-    }
+  for (int k = 0; k < 4; ++k) {
+    const bool there = slot[k] >= 0 && c < p.l.d;
+    copy_16(unit_addr(stage, tok + 2 * k, unit), from + static_cast<int64_t>(there ? slot[k] : 0) * p.l.row_bytes,
+            there);
   }
 }
 
-// Loading warps' shares ("units") of an e4m3 tile: of each channel block its
-// codes, held in the warp's registers while in flight and converted then (a
-// block with more than 4 items of 16 codes a token: its tokens' first and second
-// half apart), and its pe channels, copied as they are.
-struct UnitShape {
-  int b;       // channel block
-  int codes;   // items of 16 codes that the block has of a token
-  bool pe;     // this unit: the block's pe channels
-  int lanes;   // code units: lanes a token, 8 or 4
-  int token;   // code units: the first token
-  int weight;  // arrivals of a lane on the stage's barrier, kArrivals over the block's units
-};
-constexpr int kArrivals = 6;
-__device__ __forceinline__ int codes_of(const RowLayout& l, int b) {
-  return min(max(l.nope - b * kBlock, 0), kBlock) / 16;
-}
-__device__ __forceinline__ int units_of(const RowLayout& l, int b) {
-  const int codes = codes_of(l, b);
-  return (codes > 4 ? 2 : codes > 0 ? 1 : 0) + (min(l.d, (b + 1) * kBlock) > l.nope ? 1 : 0);
-}
-__device__ __forceinline__ UnitShape unit_shape(const RowLayout& l, int u) {
-  int b = 0, n = units_of(l, 0);
-  while (u >= n) {
-    u -= n;
-    n = units_of(l, ++b);
-  }
-  UnitShape q;
-  q.b = b;
-  q.codes = codes_of(l, b);
-  q.lanes = q.codes > 4 ? 8 : 4;
-  const int halves = q.codes > 4 ? 2 : q.codes > 0 ? 1 : 0;
-  q.pe = u >= halves;
-  q.token = 32 * u;
-  q.weight = kArrivals / n;
-  return q;
-}
-
-// The codes of a unit: of token `token` + lane / lanes + (32 / lanes) k in step
-// k the 16 codes lane % lanes, so 8 steps take half a block's tokens, or all with
-// 4 lanes each.
-struct RawCodes {
-  uint4 v[8];
-  uint32_t scales;  // the block's two scale bytes of tokens `token` + lane (low half) and + 32
+// e4m3 rows: 4 tokens a warp, 8 lanes a token, 16 codes of every block a lane.
+// A tile's codes are in registers while in flight, two tiles at a time.
+// Lanes are laid out so that 8 in a row store 4 units each of two neighbouring
+// tokens: all 32 banks.
+struct RawTile {
+  uint4 v[kMaxBlocks];
+  uint2 scales;  // the row's scale bytes
+  int slot;      // this lane's token's, -1: left out
 };
 
 __device__ __forceinline__ void load_16_if(uint4& v, const char* at, bool there) {  // 0 where it is not
@@ -360,81 +322,62 @@ __device__ __forceinline__ void load_16_if(uint4& v, const char* at, bool there)
       : "l"(at), "r"(static_cast<int>(there)));
 }
 
-__device__ __forceinline__ void load_codes(const AttnParams& p, RawCodes& raw, const UnitShape& q, const int* slots,
-                                           int lane) {
-  const int item = lane & (q.lanes - 1), first = q.token + (q.lanes == 8 ? lane >> 3 : lane >> 2);
-  const int step = q.lanes == 8 ? 4 : 8;
-  const char* from = p.cache + q.b * kBlock + 16 * item;
-  int slot[8];
+__device__ __forceinline__ void load_codes(const AttnParams& p, RawTile& raw, int nblk, int item) {
+  const bool there = raw.slot >= 0;
+  const char* row = p.cache + static_cast<int64_t>(there ? raw.slot : 0) * p.l.row_bytes;
+  raw.scales = make_uint2(0u, 0u);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "@p ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"  // rows end on a 16-byte boundary: 8 bytes are there
+      : "+r"(raw.scales.x), "+r"(raw.scales.y)
+      : "l"(row + p.l.scale_off), "r"(static_cast<int>(there)));
 #pragma unroll
-  for (int k = 0; k < 8; ++k) slot[k] = slots[first + step * k];
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    load_16_if(raw.v[k], from + static_cast<int64_t>(slot[k]) * p.l.row_bytes, slot[k] >= 0 && item < q.codes);
-  unsigned short two[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int s = k == 0 || q.lanes == 4 ? slots[q.token + lane + 32 * k] : -1;
-    if (s >= 0)  // rows end on a 16-byte boundary: two bytes are there even where one group is
-      asm volatile("ld.global.nc.u16 %0, [%1];"
-                   : "=h"(two[k])
-                   : "l"(p.cache + static_cast<int64_t>(s) * p.l.row_bytes + p.l.scale_off + 2 * q.b));
-  }
-  raw.scales = two[0] | static_cast<uint32_t>(two[1]) << 16;
+  for (int b = 0; b < kMaxBlocks; ++b)
+    if (b < nblk) {
+      const int c = b * kBlock + 16 * item;
+      load_16_if(raw.v[b], row + c, there && c < p.l.nope);
+    }
 }
 
-__device__ __forceinline__ void store_codes(const RawCodes& raw, const UnitShape& q, int lane, uint32_t stage) {
-  const int item = lane & (q.lanes - 1), first = q.lanes == 8 ? lane >> 3 : lane >> 2;
-  const int step = q.lanes == 8 ? 4 : 8;
-  const int odd = item >> 2;  // also the item's scale of the two
+// Block b's codes of this lane's token (token t of the tile) into the stage.
+__device__ __forceinline__ void store_codes(const uint4& w, const uint2& scales, int b, int item, int t,
+                                            uint32_t stage) {
+  const uint32_t two = (b & 2 ? scales.y : scales.x) >> (16 * (b & 1));
+  const uint32_t byte = (two >> (8 * (item >> 2))) & 255u;
   // 2^(byte - 127) times the 2^120 of the conversion is one bf16 factor up to a
   // scale of 2^7; above, 2^127 is, and the rest of it another.
-  const auto over = [](uint32_t byte) { return byte > 134u && byte != 255u; };
-  const uint32_t s4 = raw.scales;
-  const bool large = __any_sync(0xFFFFFFFFu, over(s4 & 255u) || over(s4 >> 8 & 255u) || over(s4 >> 16 & 255u) ||
-                                                over(s4 >> 24));
-  const uint32_t row = stage + q.token * 128;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int t = first + step * k;
-    const uint32_t two = __shfl_sync(0xFFFFFFFFu, s4, t & 31) >> (16 * (t >> 5));
-    const uint32_t byte = (two >> (8 * odd)) & 255u;
-    uint32_t f = byte == 255u ? 0x7FC0u : min(byte + 120u, 254u) << 7;
-    f |= f << 16;
-    const uint4 w = raw.v[k];
-    uint4 lo, hi;
-    latent::e4m3x4_times(w.x, f, lo.x, lo.y);
-    latent::e4m3x4_times(w.y, f, lo.z, lo.w);
-    latent::e4m3x4_times(w.z, f, hi.x, hi.y);
-    latent::e4m3x4_times(w.w, f, hi.z, hi.w);
-    if (large) {
-      const uint32_t r = latent::scale_bf16x2(over(byte) ? byte - 7u : 127u);
-      lo.x = latent::mul_bf16x2(lo.x, r), lo.y = latent::mul_bf16x2(lo.y, r);
-      lo.z = latent::mul_bf16x2(lo.z, r), lo.w = latent::mul_bf16x2(lo.w, r);
-      hi.x = latent::mul_bf16x2(hi.x, r), hi.y = latent::mul_bf16x2(hi.y, r);
-      hi.z = latent::mul_bf16x2(hi.z, r), hi.w = latent::mul_bf16x2(hi.w, r);
-    }
-    if (item < q.codes) {
-      // lanes of the two 64-channel halves write the even and the odd unit
-      // first in turn: the lanes of a token then cover all 32 banks
-      store_16(unit_addr(row, t, 2 * item + odd), odd ? hi : lo);
-      store_16(unit_addr(row, t, 2 * item + 1 - odd), odd ? lo : hi);
-    }
+  const bool over = byte > 134u && byte != 255u;
+  uint32_t f = byte == 255u ? 0x7FC0u : min(byte + 120u, 254u) << 7;
+  f |= f << 16;
+  uint4 lo, hi;
+  latent::e4m3x4_times(w.x, f, lo.x, lo.y);
+  latent::e4m3x4_times(w.y, f, lo.z, lo.w);
+  latent::e4m3x4_times(w.z, f, hi.x, hi.y);
+  latent::e4m3x4_times(w.w, f, hi.z, hi.w);
+  if (over) {
+    const uint32_t r = latent::scale_bf16x2(byte - 7u);
+    lo.x = latent::mul_bf16x2(lo.x, r), lo.y = latent::mul_bf16x2(lo.y, r);
+    lo.z = latent::mul_bf16x2(lo.z, r), lo.w = latent::mul_bf16x2(lo.w, r);
+    hi.x = latent::mul_bf16x2(hi.x, r), hi.y = latent::mul_bf16x2(hi.y, r);
+    hi.z = latent::mul_bf16x2(hi.z, r), hi.w = latent::mul_bf16x2(hi.w, r);
   }
+  store_16(unit_addr(stage, t, 2 * item), lo);
+  store_16(unit_addr(stage, t, 2 * item + 1), hi);
 }
 
-// The pe channels of a block, and zeros behind the last channel: 16 lanes take
-// a token's units of 8 channels.
-__device__ __forceinline__ void copy_pe(const AttnParams& p, const UnitShape& q, const int* slots, int lane,
+// The pe channels of block b, and zeros behind the last channel, of tokens tok
+// and tok + 2: 16 lanes take a token's units of 8 channels.
+__device__ __forceinline__ void copy_pe(const AttnParams& p, const int (&slot)[2], int b, int tok, int lane,
                                         uint32_t stage) {
-  const int unit = lane & 15, half = lane >> 4, c = q.b * kBlock + 8 * unit;
-  const bool mine = c >= p.l.nope, there = mine && c < p.l.d;
-  const char* from = p.cache + (there ? p.l.nope + 2 * (c - p.l.nope) : 0);
-#pragma unroll 8
-  for (int k = 0; k < 32; ++k) {
-    const int t = 32 * half + k, slot = slots[t];
-    const bool ok = there && slot >= 0;
-    if (mine) copy_16(unit_addr(stage, t, unit), from + static_cast<int64_t>(ok ? slot : 0) * p.l.row_bytes, ok);
+  const int unit = lane & 15, c = b * kBlock + 8 * unit;
+  if (c < p.l.nope) return;
+  const char* from = p.cache + (c < p.l.d ? p.l.nope + 2 * (c - p.l.nope) : 0);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const bool there = slot[k] >= 0 && c < p.l.d;
+    copy_16(unit_addr(stage, tok + 2 * k, unit), from + static_cast<int64_t>(there ? slot[k] : 0) * p.l.row_bytes,
+            there);
   }
 }
 
@@ -511,25 +454,16 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   volatile int* abort_flag = &ctl->abort;
   const int nblk = (p.l.d + kBlock - 1) / kBlock;
-  int units = nblk;  // loading warps' shares of a tile
-  if (E4M3) {
-    units = 0;
-    for (int b = 0; b < nblk; ++b) units += units_of(p.l, b);
-  }
-  // Loading warps take units in turn; a warp's next is at most kStages blocks and
-  // kSlotRing tiles on (kStages - 1 on average is at most one less), so that a
-  // parity tells the phase it waits for from the one two before.
-  const int load_warps = min(min(kLoadWarps<E4M3>, kSlotRing * units), (kStages - 1) * units / nblk);
   const auto bar = [](uint64_t& b) { return ptx::smem_u32(&b); };
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(bar(ctl->full[s]), E4M3 ? 32 * kArrivals : 32);
+      ptx::mbar_init(bar(ctl->full[s]), kLoadWarps<E4M3> * (E4M3 ? 33 : 32));
       ptx::mbar_init(bar(ctl->empty[s]), 1);
     }
     for (int i = 0; i < kSlotRing; ++i) {
       ptx::mbar_init(bar(ctl->slots_full[i]), 1);
-      ptx::mbar_init(bar(ctl->slots_empty[i]), units);
+      ptx::mbar_init(bar(ctl->slots_empty[i]), kLoadWarps<E4M3>);
     }
     ptx::mbar_init(bar(ctl->q_full), 1);
     ptx::mbar_init(bar(ctl->q_empty), 1);
@@ -846,9 +780,8 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       ++tile;
       return true;
     };
-    // behind the last tile, one mark for each loading warp to find
-    int marks = (load_warps - 1) / units + 1;
-    for (bool live = look_up(), ok = true; ok && (live || marks > 0); ++g) {
+    bool live = look_up(), marked = false;
+    for (bool ok = true; ok && !marked; ++g) {
       const int s0 = live ? slot_of(p, ref[0]) : kNoTile, s1 = live ? slot_of(p, ref[1]) : kNoTile;
       const bool more = live && look_up();
       const uint32_t i = g % kSlotRing;
@@ -861,48 +794,85 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       if (lane == 0 && live) ctl->mask[g % kMaskRing] = lo | static_cast<uint64_t>(hi) << 32;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_full[i]));
-      if (!live) --marks;
+      marked = !live;  // behind the last tile, the mark that there is none
       live = more;
     }
   } else {
     // ---------------------------------------------------------------- cache rows
-    // units are counted over all tiles; this warp takes every load_warps-th
-    uint32_t n = warp - kLoadWarp;
-    for (bool ok = warp - kLoadWarp < load_warps; ok; n += load_warps) {
-      const uint32_t g = n / units, u = n - g * units, i = g % kSlotRing;
+    const int v = warp - kLoadWarp;
+    uint32_t g = 0, s = 0, phase = 1;  // tiles looked up; stage, and the phase of `empty` that lets it be filled
+    bool ok = true;
+    // The slots of the next tile, read with `take`; false behind the last.
+    const auto next_slots = [&](auto take) {
+      const uint32_t i = g % kSlotRing;
+      ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(ctl->slots_full[i]), (g / kSlotRing) & 1, abort_flag, kFaultLoad));
       const int* slots = ctl->slot[i];
-      ok = wait_bar(bar(ctl->slots_full[i]), (g / kSlotRing) & 1, abort_flag, kFaultLoad);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      if (slots[0] == kNoTile) {
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_empty[i]));
-        break;
+      const bool some = slots[0] != kNoTile;
+      take(slots);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_empty[i]));
+      ++g;
+      return ok && some;
+    };
+    const auto next_stage = [&] {
+      if (++s == kStages) {
+        s = 0;
+        phase ^= 1;
       }
-      const UnitShape q = E4M3 ? unit_shape(p.l, u) : UnitShape{static_cast<int>(u), 0, true, 0, 0, 1};
-      RawCodes raw;
-      if (E4M3 && !q.pe) {
-        load_codes(p, raw, q, slots, lane);
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_empty[i]));
+    };
+    const auto wait_stage = [&] {
+      ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(ctl->empty[s]), phase, abort_flag, kFaultLoad));
+      return ok;
+    };
+    if (!E4M3) {
+      const int tok = 8 * v + (lane >> 4);
+      int slot[4];
+      while (next_slots([&](const int* slots) {
+        for (int k = 0; k < 4; ++k) slot[k] = slots[tok + 2 * k];
+      })) {
+        for (int b = 0; b < nblk; ++b) {
+          if (!wait_stage()) break;
+          copy_block(p, slot, b, tok, lane, base + kOffRing + s * kStageBytes);
+          copies_arrive(bar(ctl->full[s]));
+          next_stage();
+        }
+        if (!ok) break;
       }
-      const uint32_t block = g * nblk + q.b, s = block % kStages;
-      const uint32_t stage = base + kOffRing + s * kStageBytes;
-      // the phase of `empty` that lets the stage be filled (the one before the first counts as done)
-      ok = wait_bar(bar(ctl->empty[s]), (block / kStages + 1) & 1, abort_flag, kFaultLoad);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      if (E4M3 && !q.pe) {
-        store_codes(raw, q, lane, stage);
-        ptx::mbar_arrive_n(bar(ctl->full[s]), q.weight);
-      } else {
-        if (E4M3)
-          copy_pe(p, q, slots, lane, stage);
-        else
-          copy_block(p, slots, q.b, lane, stage);
-        for (int k = 0; k < q.weight; ++k) copies_arrive(bar(ctl->full[s]));
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(ctl->slots_empty[i]));
+    } else {
+      const int tok = 4 * v + 2 * (lane >> 4) + (lane >> 2 & 1), item = (lane >> 1 & 4) | (lane & 3);
+      RawTile one, two;
+      const auto load = [&](RawTile& raw) {
+        const bool live = next_slots([&](const int* slots) { raw.slot = slots[tok]; });
+        if (live) load_codes(p, raw, nblk, item);
+        return live;
+      };
+      const auto convert = [&](const RawTile& raw) {
+        // the slots of tokens 4 v + lane / 16 and that + 2 for the pe copies
+        int pe_slot[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) pe_slot[k] = __shfl_sync(0xFFFFFFFFu, raw.slot, 16 * k + 4 * (lane >> 4));
+#pragma unroll
+        for (int b = 0; b < kMaxBlocks; ++b) {
+          if (b >= nblk || !wait_stage()) break;
+          const uint32_t stage = base + kOffRing + s * kStageBytes;
+          if (b * kBlock + 16 * item < p.l.nope) store_codes(raw.v[b], raw.scales, b, item, tok, stage);
+          // a lane's arrival 33 times, or once with one of each lane's copies
+          const bool pe = min(p.l.d, (b + 1) * kBlock) > p.l.nope;
+          if (pe) {
+            copy_pe(p, pe_slot, b, 4 * v + (lane >> 4), lane, stage);
+            copies_arrive(bar(ctl->full[s]));
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_n(bar(ctl->full[s]), pe ? 1 : 33);
+          next_stage();
+        }
+        return ok;
+      };
+      bool live1 = load(one), live2 = live1 && load(two);
+      while (live1 && convert(one)) {
+        live1 = live2 && load(one);
+        if (!live2 || !convert(two)) break;
+        live2 = live1 && load(two);
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // nothing lands after the block has left
