@@ -428,6 +428,9 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       : "memory");
 }
 
+// A condition that is the same on all lanes, as one the compiler knows to be.
+__device__ __forceinline__ bool warp_any(bool x) { return __any_sync(0xFFFFFFFFu, x); }
+
 // True on all 128 softmax threads when it is on any of them; a barrier.
 __device__ __forceinline__ bool any_softmax(bool x) {
   uint32_t r;
@@ -664,9 +667,11 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
     if (!begun && tid == 0 && p.split) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
   } else if (warp == kScoreWarp) {
     // ---------------------------------------------------------------- queries, S
-    // The whole warp walks; an elected lane issues each batch of products from
-    // warp-uniform operands (a lone thread took 110-130 cycles an MMA to set
-    // them up, against 33 and 49 of the tensor core for S and O^T).
+    // The whole warp walks, and every branch around the products is on a vote:
+    // what the compiler can prove uniform stays in uniform registers, where an
+    // MMA takes its operands from (a lone thread, or loops on a lane's own
+    // counts, took 60-130 cycles an MMA to move them there, against 33 and 49 of
+    // the tensor core for S and O^T).
     const uint32_t id_s = ptx::idesc_bf16_f32(64, kTile, false, false);
     // operands' descriptors, to which address steps (in 16-byte units) are added
     const uint64_t q_desc = ptx::smem_desc_sw128(base + kOffQ, 16, 1024);
@@ -674,9 +679,8 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
     const int chunks = (p.l.d + 63) / 64;
     const int tail = (p.l.d - (nblk - 1) * kBlock + 15) / 16;  // K steps in the last block
     uint32_t g = 0, item = 0, s = 0, phase = 0;
-    while (w.next(p, x)) {
-      const int j0 = __shfl_sync(0xFFFFFFFFu, x.j0, 0), j1 = __shfl_sync(0xFFFFFFFFu, x.j1, 0);
-      if (j1 == j0) continue;
+    while (warp_any(w.next(p, x))) {
+      if (!warp_any(x.j1 > x.j0)) continue;
       if (item > 0) wait_bar(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultScore);
       if (ptx::elect_one()) {
         ptx::mbar_arrive_expect_tx(bar(ctl->q_full), chunks * p.tile_heads * 128);
@@ -686,29 +690,31 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       }
       __syncwarp();
       wait_bar(bar(ctl->q_full), item & 1, abort_flag, kFaultScore);
-      for (int j = j0; j < j1; ++j, ++g) {
+      for (int j = x.j0; warp_any(j < x.j1); ++j, ++g) {
         if (g >= 2) wait_bar(bar(ctl->s_empty[g & 1]), ((g >> 1) - 1) & 1, abort_flag, kFaultScore);
         const uint32_t ds = tmem + kColS + (g & 1) * 64;
+        // Blocks fill in order (a loading thread's arrivals are), so a last one
+        // that is full stands for all: their products then go out in one run,
+        // without the ~250 cycles of a wait and its fences between them.
+        const uint32_t last = s + nblk - 1, ls = last < kStages ? last : last - kStages;
+        const bool ready = warp_any(ptx::mbar_test_wait(bar(ctl->full[ls]), last < kStages ? phase : phase ^ 1));
         for (int b = 0; b < nblk; ++b) {
-          wait_bar(bar(ctl->full[s]), phase, abort_flag, kFaultScore);
-          // The loading threads' stores become visible to the tensor core by a
-          // fence on this side of the barrier: on theirs it would wait for
-          // their loads in flight, a memory latency a block.
-          ptx::fence_proxy_async_smem();
-          ptx::tc_fence_after();
+          if (!ready) wait_bar(bar(ctl->full[s]), phase, abort_flag, kFaultScore);
+          if (!ready || b == 0) {
+            // The loading threads' stores become visible to the tensor core by a
+            // fence on this side of the barrier: on theirs it would wait for
+            // their loads in flight, a memory latency a block.
+            ptx::fence_proxy_async_smem();
+            ptx::tc_fence_after();
+          }
           const uint64_t qd = q_desc + b * (16384u >> 4), cd = c_desc + s * (kStageBytes >> 4);
-          const bool last = b == nblk - 1;
+          const int steps = b == nblk - 1 ? tail : 8;
           if (ptx::elect_one()) {
             ptx::tc_mma_ss(ds, qd, cd, id_s, b > 0);
-            const int steps = last ? tail : 8;
 #pragma unroll
             for (int k = 1; k < 8; ++k) {
               const uint32_t at = ((k >> 2) * 8192u + (k & 3) * 32u) >> 4;
               if (k < steps) ptx::tc_mma_ss(ds, qd + at, cd + at, id_s, 1);
-            }
-            if (last) {
-              ptx::tc_commit(bar(ctl->s_full[g & 1]));
-              if (j == j1 - 1) ptx::tc_commit(bar(ctl->q_empty));
             }
           }
           __syncwarp();
@@ -717,6 +723,12 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
             phase ^= 1;
           }
         }
+        const bool last_tile = warp_any(j == x.j1 - 1);
+        if (ptx::elect_one()) {
+          ptx::tc_commit(bar(ctl->s_full[g & 1]));
+          if (last_tile) ptx::tc_commit(bar(ctl->q_empty));
+        }
+        __syncwarp();
       }
       ++item;
     }
@@ -732,9 +744,9 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
     const uint64_t c_desc = ptx::smem_desc_sw128(base + kOffRing, kHalf, 1024);
     const uint64_t p_desc = ptx::smem_desc_sw128(base + kOffP, 16, 1024);
     uint32_t g = 0, s = 0;
-    while (w.next(p, x)) {
-      const int tiles = __shfl_sync(0xFFFFFFFFu, x.j1 - x.j0, 0);
-      for (int j = 0; j < tiles; ++j, ++g) {
+    while (warp_any(w.next(p, x))) {
+      bool first = true;
+      for (int j = x.j0; warp_any(j < x.j1); ++j, ++g, first = false) {
         wait_bar(bar(ctl->p_full[g & 1]), (g >> 1) & 1, abort_flag, kFaultValue);
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_after();
@@ -742,7 +754,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
         for (int b = 0; b < nblk; ++b) {
           const uint64_t cd = c_desc + s * (kStageBytes >> 4);
           if (ptx::elect_one()) {
-            ptx::tc_mma_ss(tmem + b * 64, cd, pd, id_o, j > 0);
+            ptx::tc_mma_ss(tmem + b * 64, cd, pd, id_o, !first);
 #pragma unroll
             for (int k = 1; k < kTile / 16; ++k)
               ptx::tc_mma_ss(tmem + b * 64, cd + k * (2048 >> 4), pd + k * (32 >> 4), id_o, 1);
@@ -888,8 +900,12 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
 }
 
 // Adds up the partials of the rows that were split, in the order of their
-// tiles: one thread block a (row, head) at a time, a thread 4 channels.
-constexpr int kJoinThreads = latent::kMaxD / 4;
+// tiles: O = sum_k w_k part_k / sum_k w_k sum_k, w_k = 2^(reference_k - the
+// largest). A warp takes a (row, head), 4 x 128 channels; with few of them (a
+// long row over many runs) a block takes 128 channels of one, a warp every
+// fourth partial. All reads of a step are in flight at once: the time is a few
+// L2 latencies (one block a head with its loads in turn took 20-40 us).
+constexpr int kJoinWarps = 4;
 constexpr int kMaxRuns = 256;
 
 struct JoinParams {
@@ -901,15 +917,14 @@ struct JoinParams {
   int runs, nh, tile_heads, d;
 };
 
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(JoinParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(JoinParams p) {
   __shared__ int4 todo[kMaxRuns];  // (pieces, row, head tile, first run) of the split rows
-  __shared__ int count[kMaxRuns / 32];
-  __shared__ float weight[kMaxRuns];
-  __shared__ float red[kJoinThreads / 32];
+  __shared__ int count[kJoinWarps];
+  __shared__ float4 sums[kJoinWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   ptx::griddep_wait();  // launched early: wait for the partials
   int n = 0;
-  for (int c0 = 0; c0 < p.runs; c0 += kJoinThreads) {
+  for (int c0 = 0; c0 < p.runs; c0 += 32 * kJoinWarps) {
     const int c = c0 + tid;
     int4 e = make_int4(0, 0, 0, 0);
     if (c < p.runs) e = p.split[c];
@@ -917,7 +932,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(JoinParams p)
     if (lane == 0) count[warp] = __popc(some);
     __syncthreads();
     int at = n;
-    for (int k = 0; k < kJoinThreads / 32; ++k) {
+    for (int k = 0; k < kJoinWarps; ++k) {
       if (k < warp) at += count[k];
       n += count[k];
     }
@@ -927,50 +942,90 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(JoinParams p)
     }
     __syncthreads();
   }
-  const int units = n * p.tile_heads;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int4 e = todo[u / p.tile_heads];
-    const int h = u % p.tile_heads, head = e.z * p.tile_heads + h;
-    if (head >= p.nh) continue;
+  const int heads = n * p.tile_heads, quarters = (p.d + 127) / 128;
+  const bool wide = heads * quarters <= static_cast<int>(gridDim.x);  // a block to a quarter of a head
+  const int units = wide ? heads * quarters : heads;
+  const int per = wide ? 1 : kJoinWarps;
+  for (int u0 = blockIdx.x * per; u0 < units; u0 += gridDim.x * per) {
+    const int u = wide ? u0 : u0 + warp;
+    const int unit = wide ? u / quarters : u, q0 = wide ? u - unit * quarters : 0, q1 = wide ? q0 + 1 : quarters;
+    const int4 e = u < units ? todo[unit / p.tile_heads] : make_int4(0, 0, 0, 0);
+    const int h = unit % p.tile_heads, head = e.z * p.tile_heads + h;
+    const bool live = u < units && head < p.nh;
+    const int pieces = live ? e.x : 0;
     const auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * e.w : 2 * (e.w + k) + 1) * p.tile_heads + h; };
     float top = -INFINITY;
-    for (int k = tid; k < e.x; k += kJoinThreads) top = fmaxf(top, p.part_ml[slot(k)].x);
+    for (int k = lane; k < pieces; k += 32) top = fmaxf(top, p.part_ml[slot(k)].x);
     for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if (lane == 0) red[warp] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    __syncthreads();
+    const float ref = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
-    for (int k = tid; k < e.x; k += kJoinThreads) {
+    for (int k = lane; k < pieces; k += 32) {
       const float2 ml = p.part_ml[slot(k)];
-      const float w = top == -INFINITY ? 0.f : exp2_fast(ml.x - top);
-      weight[k] = w;
-      sum += w * ml.y;
+      sum += exp2_fast(ml.x - ref) * ml.y;
     }
     for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) red[warp] = sum;
-    __syncthreads();
-    sum = (red[0] + red[1]) + (red[2] + red[3]);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t out = static_cast<int64_t>(e.y) * p.nh + head;
-    if (tid * 4 < p.d) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    // partials k0, k0 + step, ... of channels 128 q + 4 lane and on
+    const auto add = [&](float4& acc, int k0, int step, int q) {
+      const int c = 128 * q + 4 * lane;
 #pragma unroll 8
-      for (int k = 0; k < e.x; ++k) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part + slot(k) * p.d) + tid);
-        const float w = weight[k];
-        acc.x += w * v.x;
-        acc.y += w * v.y;
-        acc.z += w * v.z;
-        acc.w += w * v.w;
+      for (int k = k0; k < pieces; k += step) {
+        const float w = exp2_fast(__ldg(&p.part_ml[slot(k)].x) - ref);
+        if (c < p.d) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(p.part + slot(k) * p.d + c));
+          acc.x += w * v.x;
+          acc.y += w * v.y;
+          acc.z += w * v.z;
+          acc.w += w * v.w;
+        }
       }
-      uint2 o;
-      o.x = ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
-      o.y = ptx::pack_bf16x2(acc.z * inv, acc.w * inv);
-      *reinterpret_cast<uint2*>(p.O + out * p.d + tid * 4) = o;
+    };
+    const auto store = [&](const float4& acc, int q) {
+      const int c = 128 * q + 4 * lane;
+      if (live && c < p.d) {
+        uint2 o;
+        o.x = ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
+        o.y = ptx::pack_bf16x2(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(p.O + out * p.d + c) = o;
+      }
+    };
+    if (wide) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      add(acc, warp, kJoinWarps, q0);
+      sums[warp][lane] = acc;
+      __syncthreads();
+      if (warp == 0) {
+        for (int k = 1; k < kJoinWarps; ++k) {
+          const float4 v = sums[k][lane];
+          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
+        store(acc, q0);
+      }
+      __syncthreads();
+    } else {
+      float4 acc[kMaxBlocks] = {};
+#pragma unroll 4
+      for (int k = 0; k < pieces; ++k) {
+        const float w = exp2_fast(__ldg(&p.part_ml[slot(k)].x) - ref);
+#pragma unroll
+        for (int q = 0; q < kMaxBlocks; ++q) {
+          const int c = 128 * q + 4 * lane;
+          if (c < p.d) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(p.part + slot(k) * p.d + c));
+            acc[q].x += w * v.x;
+            acc[q].y += w * v.y;
+            acc[q].z += w * v.z;
+            acc[q].w += w * v.w;
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kMaxBlocks; ++q)
+        if (q < q1) store(acc[q], q);
     }
-    if (p.lse && tid == 0) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-    __syncthreads();  // weight and red are read
+    if (live && p.lse && lane == 0 && q0 == 0 && (!wide || warp == 0))
+      p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
   }
 }
 
@@ -1096,8 +1151,8 @@ int attend(AttnParams& p, const void* q, void* workspace, size_t workspace_bytes
   // attention drains; its blocks wait in-kernel for the partials
   const JoinParams jp{p.part, p.part_ml, p.split, p.O, p.lse, n.grid, p.nh, n.tile_heads, p.l.d};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(dev.sms * 2));
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(dev.sms * 8));
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
