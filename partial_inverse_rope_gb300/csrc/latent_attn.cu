@@ -20,10 +20,10 @@
 // warp each: either product goes out as soon as what it needs is there, so a
 // late tile does not hold up the one that frees its stages), 6 the tokens'
 // cache slots, 7 the fence between loading threads' stores and the tensor core,
-// from 8 on cache rows. bf16 rows go straight to shared memory: whole pieces of
-// pages by TMA, other rows by cp.async. e4m3 rows are held in registers while in
-// flight (the ring of bf16 tiles leaves no shared memory for them) and converted
-// on the way.
+// from 8 on cache rows. bf16 rows go straight to shared memory (cp.async: boxes
+// of 128 bytes by row went no faster than 4.4 TB/s through TMA, 16 bytes a thread
+// 6.6). e4m3 rows are held in registers while in flight (the ring of bf16 tiles
+// leaves no shared memory for them) and converted on the way.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -104,7 +104,6 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct AttnParams {
   CUtensorMap tm_q;      // [rows][nh][d], boxes of [1][heads of a tile][64]
-  CUtensorMap tm_c;      // bf16 cache [slots][d], boxes of [box_rows][64]
   const char* cache;
   const int32_t* table;  // page table [rows, width] or index table [rows, width]
   const int32_t* lens;   // NULL: an index table
@@ -118,7 +117,6 @@ struct AttnParams {
   int64_t rows, width, num_slots;
   int num_pages;         // entries of an index table are pages of one slot
   int nh, head_tiles, tile_heads, page_size;
-  int box_rows;          // slots that always lie together, 8 to 64; 0: rows come one by one
   float scale_log2;      // scale * log2(e)
   RowLayout l;
 };
@@ -448,22 +446,6 @@ __device__ __forceinline__ bool any_softmax(bool x) {
   return r != 0;
 }
 
-// The softmax threads clear the rows of a tile whose tokens are left out; S has
-// been taken. The caller's fence and arrival order it before O^T's products.
-__device__ __noinline__ void clear_rows(Ctl* ctl, uint64_t mask, uint32_t n0, int nblk,
-                                        uint32_t base, int tid, volatile int* abort_flag) {
-  for (int b = 0; b < nblk; ++b) {  // the copies have landed, seen from here too
-    const uint32_t n = n0 + b;
-    wait_bar(ptx::smem_u32(&ctl->full[n % kStages]), (n / kStages) & 1, abort_flag, kFaultSoftmax);
-  }
-  const int unit = tid & 15, group = tid >> 4;  // 8 rows at a time, 16 bytes of a block's 256 a thread
-  for (int t = group; t < kTile; t += 8) {
-    if (mask >> t & 1) continue;
-    for (int b = 0; b < nblk; ++b)
-      store_16(unit_addr(base + kOffRing + (n0 + b) % kStages * kStageBytes, t, unit), make_uint4(0u, 0u, 0u, 0u));
-  }
-}
-
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(1024) char smem[];
@@ -476,18 +458,17 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   volatile int* abort_flag = &ctl->abort;
   const int nblk = (p.l.d + kBlock - 1) / kBlock;
-  const bool tma = !E4M3 && p.box_rows > 0;
   const auto bar = [](uint64_t& b) { return ptx::smem_u32(&b); };
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(bar(ctl->full[s]), tma ? 1 : kLoadWarps<E4M3> * (E4M3 ? 33 : 32));
+      ptx::mbar_init(bar(ctl->full[s]), kLoadWarps<E4M3> * (E4M3 ? 33 : 32));
       ptx::mbar_init(bar(ctl->fenced[s]), 1);
       ptx::mbar_init(bar(ctl->empty[s]), 1);
     }
     for (int i = 0; i < kSlotRing; ++i) {
       ptx::mbar_init(bar(ctl->slots_full[i]), 1);
-      ptx::mbar_init(bar(ctl->slots_empty[i]), tma ? nblk : kLoadWarps<E4M3>);
+      ptx::mbar_init(bar(ctl->slots_empty[i]), kLoadWarps<E4M3>);
     }
     ptx::mbar_init(bar(ctl->q_full), 1);
     ptx::mbar_init(bar(ctl->q_empty), 1);
@@ -572,9 +553,6 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
           if ((lane & 3) == 0) ctl->factor[g & 1][hq + 8 * i] = f;
           ref[i] = m[i] == -INFINITY ? 0.f : m[i];
         }
-        // TMA brought whole pieces of pages: what is not attended to is cleared
-        // (it may be a NaN, and 0 times that is one)
-        if (tma && ~mask != 0) clear_rows(ctl, mask, n0, nblk, base, tid, abort_flag);
         // the weights of two tiles before are read
         if (g >= 2) wait_bar(bar(ctl->o_done[g & 1]), ((g >> 1) - 1) & 1, abort_flag, kFaultSoftmax);
         const uint32_t pt = base + kOffP + (g & 1) * 8192u;
@@ -697,7 +675,6 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
     // counts, took 60-130 cycles an MMA to move them there, against 33 and 49 of
     // the tensor core for S and O^T).
     const uint32_t id_s = ptx::idesc_bf16_f32(64, kTile, false, false);
-    uint64_t* ready = tma ? ctl->full : ctl->fenced;  // TMA writes need no fence
     // operands' descriptors, to which address steps (in 16-byte units) are added
     const uint64_t q_desc = ptx::smem_desc_sw128(base + kOffQ, 16, 1024);
     const uint64_t c_desc = ptx::smem_desc_sw128(base + kOffRing, 16, 1024);
@@ -719,7 +696,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
         if (g >= 2) wait_bar(bar(ctl->s_empty[g & 1]), ((g >> 1) - 1) & 1, abort_flag, kFaultScore);
         const uint32_t ds = tmem + kColS + (g & 1) * 64;
         for (int b = 0; b < nblk; ++b) {
-          wait_bar(bar(ready[s]), phase, abort_flag, kFaultScore);
+          wait_bar(bar(ctl->fenced[s]), phase, abort_flag, kFaultScore);
           ptx::tc_fence_after();
           const uint64_t qd = q_desc + b * (16384u >> 4), cd = c_desc + s * (kStageBytes >> 4);
           const int steps = b == nblk - 1 ? tail : 8;
@@ -790,20 +767,18 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
     // fence after the barrier. On the loading threads' side it would wait for
     // their loads in flight, a memory latency a block; in the warp that issues S
     // it took 130 cycles between a block's products and the next one's.
-    if (!tma) {
-      uint32_t s = 0, phase = 0;
-      while (w.next(p, x))
-        for (int j = (x.j1 - x.j0) * nblk; j > 0; --j) {
-          wait_bar(bar(ctl->full[s]), phase, abort_flag, kFaultFence);
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(ctl->fenced[s]));
-          if (++s == kStages) {
-            s = 0;
-            phase ^= 1;
-          }
+    uint32_t s = 0, phase = 0;
+    while (w.next(p, x))
+      for (int j = (x.j1 - x.j0) * nblk; j > 0; --j) {
+        wait_bar(bar(ctl->full[s]), phase, abort_flag, kFaultFence);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(ctl->fenced[s]));
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1;
         }
-    }
+      }
   } else if (warp == kTokenWarp) {
     // ---------------------------------------------------------------- slots and masks
     // A lane takes tokens lane and lane + 32 of each tile; table entries are
@@ -870,29 +845,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(ctl->empty[s]), phase, abort_flag, kFaultLoad));
       return ok;
     };
-    if (tma) {
-      // one block of every tile a warp: two boxes of 64 channels for each piece
-      // of a page, a piece a pair of lanes. What a piece holds beyond the row's
-      // length, and a piece that is left out, is cleared before it counts.
-      if (v < nblk) {
-        const int chunk = (lane >> 1) * p.box_rows, c = v * kBlock + 64 * (lane & 1);
-        const bool mine = chunk < kTile && c < p.l.d;
-        int slot = -1;
-        while (next_slots([&](const int* slots) { slot = mine ? slots[chunk] : -1; })) {
-          const uint32_t n = (g - 1) * nblk + v;
-          s = n % kStages;
-          phase = (n / kStages + 1) & 1;
-          if (!wait_stage()) break;
-          const uint32_t some = __ballot_sync(0xFFFFFFFFu, slot >= 0);
-          if (lane == 0)
-            ptx::mbar_arrive_expect_tx(bar(ctl->full[s]), __popc(some) * p.box_rows * 128);
-          __syncwarp();
-          if (slot >= 0)
-            ptx::tma_load_2d(base + kOffRing + s * kStageBytes + (lane & 1) * kHalf + chunk * 128, &p.tm_c, c, slot,
-                             bar(ctl->full[s]));
-        }
-      }
-    } else if (!E4M3) {
+    if (!E4M3) {
       const int tok = 8 * v + (lane >> 4);
       int slot[4];
       while (next_slots([&](const int* slots) {
@@ -1113,20 +1066,6 @@ bool query_map(CUtensorMap* m, const void* q, int64_t rows, int nh, int d, int t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A bf16 cache [slots][d] in boxes of box_rows rows and 64 channels; channels
-// past d read as zero.
-bool cache_map(CUtensorMap* m, const void* cache, int64_t slots, int d, int box_rows) {
-  const auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(slots)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(cache), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // How a call is cut: head tiles, thread blocks, and the workspace's parts.
 struct Plan {
   int head_tiles, tile_heads, grid;
@@ -1212,14 +1151,6 @@ int attend(AttnParams& p, const void* q, void* workspace, size_t workspace_bytes
   p.head_tiles = n.head_tiles;
   p.tile_heads = n.tile_heads;
   if (!opt_in_smem(dev.device) || !query_map(&p.tm_q, q, p.rows, p.nh, p.l.d, n.tile_heads)) return INVROPE_ERR_CUDA;
-  // Slots lie together by the largest power of two that divides the page (a
-  // tile begins on a multiple of it); from 8 rows on a box is a whole number of
-  // swizzle atoms.
-  if (fmt == KV_LATENT_BF16 && p.lens && p.page_size % 8 == 0) {
-    p.box_rows = 8;
-    while (p.box_rows < kTile && p.page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
-    if (!cache_map(&p.tm_c, p.cache, p.num_slots, p.l.d, p.box_rows)) return INVROPE_ERR_CUDA;
-  }
   if (fmt == KV_LATENT_E4M3)
     latent_attn_kernel<true><<<n.grid, kThreads<true>, kSmem, s>>>(p);
   else
