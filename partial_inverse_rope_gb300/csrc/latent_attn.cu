@@ -98,6 +98,7 @@ enum : unsigned {
   kFaultSoftmax = 0xD01,
   kFaultToken = 0xE01,
   kFaultFence = 0xE02,
+  kFaultTmem = 0xF02,  // TMEM does not begin at column 0
   kFaultSmem = 0xF01  // shared memory does not begin on a 1024-byte boundary
 };
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -137,6 +138,24 @@ __device__ __noinline__ bool wait_bar_on(uint32_t bar, uint32_t parity, volatile
 }
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned code) {
   return ptx::mbar_try_wait(bar, parity) || wait_bar_on(bar, parity, abort_flag, code);
+}
+
+// The same without a call: uniform registers, where an MMA takes its operands
+// from, do not outlive one.
+__device__ __forceinline__ void wait_bar_here(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned code) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 0; !ptx::mbar_try_wait(bar, parity); ++n) {
+    if (*abort_flag) return;
+    if ((n & 63u) != 0) continue;
+    const uint64_t t = ptx::globaltimer_ns();
+    if (n == 0) {
+      t0 = t;
+    } else if (t - t0 > kWaitLimitNs) {
+      atomicCAS(&g_latent_fault, 0u, code);
+      *abort_flag = 1;
+      return;
+    }
+  }
 }
 
 // Bounded wait that ignores the abort flag: for what must land before the
@@ -492,7 +511,13 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  // All 512 columns are this block's, so the first is column 0: a constant to
+  // the MMAs.
+  constexpr uint32_t tmem = 0;
+  if (ctl->tmem != tmem) {  // never
+    if (tid == 0) atomicCAS(&g_latent_fault, 0u, static_cast<unsigned>(kFaultTmem));
+    w.hi = w.at = 0;  // no tiles
+  }
   Piece x;
 
   if (warp < kScoreWarp) {
@@ -679,11 +704,11 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
     const uint64_t q_desc = ptx::smem_desc_sw128(base + kOffQ, 16, 1024);
     const uint64_t c_desc = ptx::smem_desc_sw128(base + kOffRing, 16, 1024);
     const int chunks = (p.l.d + 63) / 64;
-    const int tail = (p.l.d - (nblk - 1) * kBlock + 15) / 16;  // K steps in the last block
+    const bool even = (p.l.d + 63) / 64 % 2 == 0;  // the last block has both its 64-channel halves
     uint32_t g = 0, item = 0, s = 0, phase = 0;
     while (warp_any(w.next(p, x))) {
       if (!warp_any(x.j1 > x.j0)) continue;
-      if (item > 0) wait_bar(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultScore);
+      if (item > 0) wait_bar_here(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultScore);
       if (ptx::elect_one()) {
         ptx::mbar_arrive_expect_tx(bar(ctl->q_full), chunks * p.tile_heads * 128);
         for (int c = 0; c < chunks; ++c)
@@ -691,21 +716,23 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
                            static_cast<int>(x.row), bar(ctl->q_full));
       }
       __syncwarp();
-      wait_bar(bar(ctl->q_full), item & 1, abort_flag, kFaultScore);
+      wait_bar_here(bar(ctl->q_full), item & 1, abort_flag, kFaultScore);
       for (int j = x.j0; warp_any(j < x.j1); ++j, ++g) {
-        if (g >= 2) wait_bar(bar(ctl->s_empty[g & 1]), ((g >> 1) - 1) & 1, abort_flag, kFaultScore);
+        if (g >= 2) wait_bar_here(bar(ctl->s_empty[g & 1]), ((g >> 1) - 1) & 1, abort_flag, kFaultScore);
         const uint32_t ds = tmem + kColS + (g & 1) * 64;
+#pragma unroll 1
         for (int b = 0; b < nblk; ++b) {
-          wait_bar(bar(ctl->fenced[s]), phase, abort_flag, kFaultScore);
+          wait_bar_here(bar(ctl->fenced[s]), phase, abort_flag, kFaultScore);
           ptx::tc_fence_after();
           const uint64_t qd = q_desc + b * (16384u >> 4), cd = c_desc + s * (kStageBytes >> 4);
-          const int steps = b == nblk - 1 ? tail : 8;
+          const bool two = b < nblk - 1 || even;  // 64-channel halves, of four K steps
           if (ptx::elect_one()) {
-            ptx::tc_mma_ss(ds, qd, cd, id_s, b > 0);
 #pragma unroll
-            for (int k = 1; k < 8; ++k) {
-              const uint32_t at = ((k >> 2) * 8192u + (k & 3) * 32u) >> 4;
-              if (k < steps) ptx::tc_mma_ss(ds, qd + at, cd + at, id_s, 1);
+            for (int i = 0; i < 4; ++i) ptx::tc_mma_ss(ds, qd + 2 * i, cd + 2 * i, id_s, i + b > 0);
+            if (two) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                ptx::tc_mma_ss(ds, qd + (8192 >> 4) + 2 * i, cd + (kHalf >> 4) + 2 * i, id_s, 1);
             }
           }
           __syncwarp();
@@ -738,7 +765,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
     while (warp_any(w.next(p, x))) {
       bool first = true;
       for (int j = x.j0; warp_any(j < x.j1); ++j, ++g, first = false) {
-        wait_bar(bar(ctl->p_full[g & 1]), (g >> 1) & 1, abort_flag, kFaultValue);
+        wait_bar_here(bar(ctl->p_full[g & 1]), (g >> 1) & 1, abort_flag, kFaultValue);
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_after();
         const uint64_t pd = p_desc + (g & 1) * (8192u >> 4);
@@ -878,7 +905,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
           const uint32_t stage = base + kOffRing + s * kStageBytes;
           if (b * kBlock + 16 * item < p.l.nope) store_codes(raw.v[b], raw.scales, b, item, tok, stage);
           // a lane's arrival 33 times, or once with one of each lane's copies
-          const bool pe = min(p.l.d, (b + 1) * kBlock) > p.l.nope;
+          const bool pe = (b + 1) * kBlock > p.l.nope;
           if (pe) {
             copy_pe(p, pe_slot, b, 4 * v + (lane >> 4), lane, stage);
             copies_arrive(bar(ctl->full[s]));
@@ -904,7 +931,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
   __syncthreads();
   if (warp == kScoreWarp) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, kTmemCols);
+    ptx::tmem_dealloc(ctl->tmem, kTmemCols);
   }
 }
 
