@@ -16,10 +16,10 @@
 // over several blocks leaves one partial (accumulators, reference and sum in
 // fp32) for each, which latent_join_kernel adds up in a fixed order.
 //
-// Warps: 0-3 softmax and output (TMEM lanes), 4 queries (TMA) and S, 5 O^T (a
-// warp each: either product goes out as soon as what it needs is there, so a
-// late tile does not hold up the one that frees its stages), 6 the tokens'
-// cache slots, 7 the fence between loading threads' stores and the tensor core,
+// Warps: 0-3 softmax and output (TMEM lanes), 4 queries (TMA) and S of even tiles,
+// 5 S of odd tiles (one issues while the other waits, so that the tensor core
+// does not), 6 O^T (either product goes out as soon as what it needs is there: a
+// late tile does not hold up the one that frees its stages), 7 the tokens' slots,
 // from 8 on cache rows. bf16 rows go straight to shared memory (cp.async: boxes
 // of 128 bytes by row went no faster than 4.4 TB/s through TMA, 16 bytes a thread
 // 6.6). e4m3 rows are held in registers while in flight (the ring of bf16 tiles
@@ -57,7 +57,7 @@ constexpr int kOverhead = 2;     // what a row costs beside its tiles, in tiles
 constexpr int kMinUnits = 4;     // units of the line a thread block takes at least
 
 constexpr int kSoftmaxThreads = 128;
-constexpr int kScoreWarp = 4, kValueWarp = 5, kTokenWarp = 6, kFenceWarp = 7, kLoadWarp = 8;
+constexpr int kScoreWarp = 4, kValueWarp = 6, kTokenWarp = 7, kLoadWarp = 8;
 template <bool E4M3>
 constexpr int kLoadWarps = E4M3 ? 16 : 8;
 template <bool E4M3>
@@ -70,9 +70,9 @@ constexpr int kOffRing = kOffQ + latent::kMaxD * 128;       // kStages x 2 x [64
 constexpr int kOffP = kOffRing + kStages * kStageBytes;     // 2 x [64 heads][64 tokens]
 constexpr int kOffCtl = kOffP + 2 * 64 * 128;
 struct Ctl {
-  uint64_t full[kStages], fenced[kStages], empty[kStages];
+  uint64_t full[kStages], empty[kStages];
   uint64_t slots_full[kSlotRing], slots_empty[kSlotRing];
-  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], drained[2];
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], drained[3];
   uint64_t mask[kMaskRing];     // bit t: token t of the tile is attended to
   int slot[kSlotRing][kTile];   // -1: left out; kNoTile: no more tiles
   float factor[2][64];
@@ -97,7 +97,6 @@ enum : unsigned {
   kFaultValue = 0xC01,
   kFaultSoftmax = 0xD01,
   kFaultToken = 0xE01,
-  kFaultFence = 0xE02,
   kFaultTmem = 0xF02,  // TMEM does not begin at column 0
   kFaultSmem = 0xF01  // shared memory does not begin on a 1024-byte boundary
 };
@@ -482,7 +481,6 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(bar(ctl->full[s]), kLoadWarps<E4M3> * (E4M3 ? 33 : 32));
-      ptx::mbar_init(bar(ctl->fenced[s]), 1);
       ptx::mbar_init(bar(ctl->empty[s]), 1);
     }
     for (int i = 0; i < kSlotRing; ++i) {
@@ -490,7 +488,8 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       ptx::mbar_init(bar(ctl->slots_empty[i]), kLoadWarps<E4M3>);
     }
     ptx::mbar_init(bar(ctl->q_full), 1);
-    ptx::mbar_init(bar(ctl->q_empty), 1);
+    ptx::mbar_init(bar(ctl->q_empty), 2);
+    ptx::mbar_init(bar(ctl->drained[2]), 1);
     for (int k = 0; k < 2; ++k) {
       ptx::mbar_init(bar(ctl->s_full[k]), 1);
       ptx::mbar_init(bar(ctl->s_empty[k]), kSoftmaxThreads);
@@ -692,7 +691,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       ptx::tc_fence_before();  // the next row's products overwrite O^T after this thread's next weights
     }
     if (!begun && tid == 0 && p.split) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
-  } else if (warp == kScoreWarp) {
+  } else if (warp < kValueWarp) {
     // ---------------------------------------------------------------- queries, S
     // The whole warp walks, and every branch around the products is on a vote:
     // what the compiler can prove uniform stays in uniform registers, where an
@@ -705,24 +704,33 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
     const uint64_t c_desc = ptx::smem_desc_sw128(base + kOffRing, 16, 1024);
     const int chunks = (p.l.d + 63) / 64;
     const bool even = (p.l.d + 63) / 64 % 2 == 0;  // the last block has both its 64-channel halves
-    uint32_t g = 0, item = 0, s = 0, phase = 0;
+    const uint32_t mine = warp - kScoreWarp;  // tiles g with g % 2 == mine
+    uint32_t g = 0, item = 0;
     while (warp_any(w.next(p, x))) {
       if (!warp_any(x.j1 > x.j0)) continue;
-      if (item > 0) wait_bar_here(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultScore);
-      if (ptx::elect_one()) {
-        ptx::mbar_arrive_expect_tx(bar(ctl->q_full), chunks * p.tile_heads * 128);
-        for (int c = 0; c < chunks; ++c)
-          ptx::tma_load_3d(base + kOffQ + c * 8192u, &p.tm_q, c * 64, x.head_tile * p.tile_heads,
-                           static_cast<int>(x.row), bar(ctl->q_full));
+      if (mine == 0) {
+        if (item > 0) wait_bar_here(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultScore);
+        if (ptx::elect_one()) {
+          ptx::mbar_arrive_expect_tx(bar(ctl->q_full), chunks * p.tile_heads * 128);
+          for (int c = 0; c < chunks; ++c)
+            ptx::tma_load_3d(base + kOffQ + c * 8192u, &p.tm_q, c * 64, x.head_tile * p.tile_heads,
+                             static_cast<int>(x.row), bar(ctl->q_full));
+        }
       }
       __syncwarp();
       wait_bar_here(bar(ctl->q_full), item & 1, abort_flag, kFaultScore);
       for (int j = x.j0; warp_any(j < x.j1); ++j, ++g) {
+        if ((g & 1) != mine) continue;
         if (g >= 2) wait_bar_here(bar(ctl->s_empty[g & 1]), ((g >> 1) - 1) & 1, abort_flag, kFaultScore);
-        const uint32_t ds = tmem + kColS + (g & 1) * 64;
+        const uint32_t ds = kColS + mine * 64, n0 = g * nblk;
+        uint32_t s = n0 % kStages, phase = n0 / kStages & 1;
 #pragma unroll 1
         for (int b = 0; b < nblk; ++b) {
-          wait_bar_here(bar(ctl->fenced[s]), phase, abort_flag, kFaultScore);
+          wait_bar_here(bar(ctl->full[s]), phase, abort_flag, kFaultScore);
+          // The loading threads' stores and copies become visible to the tensor
+          // core by a fence on this side of the barrier: on theirs it would wait
+          // for their loads in flight, a memory latency a block.
+          ptx::fence_proxy_async_smem();
           ptx::tc_fence_after();
           const uint64_t qd = q_desc + b * (16384u >> 4), cd = c_desc + s * (kStageBytes >> 4);
           const bool two = b < nblk - 1 || even;  // 64-channel halves, of four K steps
@@ -741,20 +749,18 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
             phase ^= 1;
           }
         }
-        const bool last_tile = warp_any(j == x.j1 - 1);
-        if (ptx::elect_one()) {
-          ptx::tc_commit(bar(ctl->s_full[g & 1]));
-          if (last_tile) ptx::tc_commit(bar(ctl->q_empty));
-        }
+        if (ptx::elect_one()) ptx::tc_commit(bar(ctl->s_full[mine]));
         __syncwarp();
       }
+      if (ptx::elect_one()) ptx::tc_commit(bar(ctl->q_empty));  // this warp's products with these queries
+      __syncwarp();
       ++item;
     }
     // nothing may be in flight when the thread block leaves
     if (item > 0) wait_bar_noabort(bar(ctl->q_full), (item - 1) & 1);
-    if (ptx::elect_one()) ptx::tc_commit(bar(ctl->drained[0]));
+    if (ptx::elect_one()) ptx::tc_commit(bar(ctl->drained[mine]));
     __syncwarp();
-    wait_bar_noabort(bar(ctl->drained[0]), 0);
+    wait_bar_noabort(bar(ctl->drained[mine]), 0);
     __syncwarp();
   } else if (warp == kValueWarp) {
     // ---------------------------------------------------------------- O^T += C^T P^T
@@ -784,28 +790,10 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
         }
       }
     }
-    if (ptx::elect_one()) ptx::tc_commit(bar(ctl->drained[1]));
+    if (ptx::elect_one()) ptx::tc_commit(bar(ctl->drained[2]));
     __syncwarp();
-    wait_bar_noabort(bar(ctl->drained[1]), 0);
+    wait_bar_noabort(bar(ctl->drained[2]), 0);
     __syncwarp();
-  } else if (warp == kFenceWarp) {
-    // ---------------------------------------------------------------- fence
-    // Stores (and cp.async copies) become visible to the tensor core by a proxy
-    // fence after the barrier. On the loading threads' side it would wait for
-    // their loads in flight, a memory latency a block; in the warp that issues S
-    // it took 130 cycles between a block's products and the next one's.
-    uint32_t s = 0, phase = 0;
-    while (w.next(p, x))
-      for (int j = (x.j1 - x.j0) * nblk; j > 0; --j) {
-        wait_bar(bar(ctl->full[s]), phase, abort_flag, kFaultFence);
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(ctl->fenced[s]));
-        if (++s == kStages) {
-          s = 0;
-          phase ^= 1;
-        }
-      }
   } else if (warp == kTokenWarp) {
     // ---------------------------------------------------------------- slots and masks
     // A lane takes tokens lane and lane + 32 of each tile; table entries are
