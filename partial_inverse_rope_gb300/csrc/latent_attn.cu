@@ -16,14 +16,18 @@
 // over several blocks leaves one partial (accumulators, reference and sum in
 // fp32) for each, which latent_join_kernel adds up in a fixed order.
 //
-// Warps: 0-3 softmax and output (TMEM lanes), 4 queries (TMA) and S of even tiles,
-// 5 S of odd tiles (one issues while the other waits, so that the tensor core
-// does not), 6 O^T (either product goes out as soon as what it needs is there: a
-// late tile does not hold up the one that frees its stages), 7 the tokens' slots,
-// from 8 on cache rows. bf16 rows go straight to shared memory (cp.async: boxes
-// of 128 bytes by row went no faster than 4.4 TB/s through TMA, 16 bytes a thread
-// 6.6). e4m3 rows are held in registers while in flight (the ring of bf16 tiles
-// leaves no shared memory for them) and converted on the way.
+// bf16 rows go straight to shared memory (cp.async: boxes of 128 bytes by row
+// went no faster than 4.4 TB/s through TMA, 16 bytes a thread 6.6); 256 channels
+// of the queries then lie in TMEM, which leaves the ring nearly three tiles (two
+// let a tile's loads begin when the one two before was done: 5% slower). e4m3 rows
+// are held in registers while in flight and converted on the way, by more warps,
+// which leaves no registers for that.
+//
+// Warps: 0-3 softmax and output (TMEM lanes), 4 S of even tiles, 5 S of odd tiles
+// (one issues while the other waits, so that the tensor core does not), 6 O^T
+// (either product goes out as soon as what it needs is there: a late tile does not
+// hold up the one that frees its stages), 7 the tokens' slots, then with bf16 rows
+// 4 for the queries in TMEM, and those that load rows.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -48,7 +52,6 @@ using latent::RowLayout;
 constexpr int kTile = 64;        // tokens per tile
 constexpr int kBlock = 128;      // channels per stage of the ring
 constexpr int kMaxBlocks = latent::kMaxD / kBlock;
-constexpr int kStages = 9;       // two tiles of 512 channels and one stage more
 constexpr int kStageBytes = kTile * kBlock * 2;
 constexpr int kHalf = kTile * 128;       // one 64-channel half of a stage
 constexpr int kSlotRing = 4;     // tiles whose slots are looked up ahead of their loads
@@ -57,20 +60,29 @@ constexpr int kOverhead = 2;     // what a row costs beside its tiles, in tiles
 constexpr int kMinUnits = 4;     // units of the line a thread block takes at least
 
 constexpr int kSoftmaxThreads = 128;
-constexpr int kScoreWarp = 4, kValueWarp = 6, kTokenWarp = 7, kLoadWarp = 8;
+constexpr int kScoreWarp = 4, kValueWarp = 6, kTokenWarp = 7;
+constexpr int kQueryChunk = 64 * 128;    // [64 heads][64 channels]
 template <bool E4M3>
-constexpr int kLoadWarps = E4M3 ? 16 : 8;
-template <bool E4M3>
-constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps<E4M3>);
-constexpr int kMaxWarps = kLoadWarp + 16;
-
-// shared memory, from a 1024-byte boundary
-constexpr int kOffQ = 0;                                    // 8 x [64 heads][64 channels]
-constexpr int kOffRing = kOffQ + latent::kMaxD * 128;       // kStages x 2 x [64 tokens][64 channels]
-constexpr int kOffP = kOffRing + kStages * kStageBytes;     // 2 x [64 heads][64 tokens]
+struct Cfg {
+  static constexpr int kQueryBlocks = E4M3 ? 0 : 2;  // 128-channel blocks of the queries in TMEM, two bf16 a column
+  static constexpr int kStages = E4M3 ? 9 : 11;      // a tile is up to 4
+  static constexpr int kQueryWarp = 8;
+  static constexpr int kLoadWarp = E4M3 ? 8 : 12;
+  static constexpr int kLoadWarps = E4M3 ? 16 : 8;
+  static constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+  // shared memory, from a 1024-byte boundary: the other blocks of the queries,
+  // the ring (stages of 2 x [64 tokens][64 channels])
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffRing = (kMaxBlocks - kQueryBlocks) * 2 * kQueryChunk;
+  static constexpr int kEnd = kOffRing + kStages * kStageBytes;
+};
+constexpr int kMaxStages = Cfg<false>::kStages;
+constexpr int kMaxWarps = Cfg<true>::kThreads / 32;
+static_assert(Cfg<false>::kEnd == Cfg<true>::kEnd, "both fill the same shared memory");
+constexpr int kOffP = Cfg<false>::kEnd;                     // 2 x [64 heads][64 tokens]
 constexpr int kOffCtl = kOffP + 2 * 64 * 128;
 struct Ctl {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t slots_full[kSlotRing], slots_empty[kSlotRing];
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], drained[3];
   uint64_t mask[kMaskRing];     // bit t: token t of the tile is attended to
@@ -88,7 +100,9 @@ constexpr int kSmem = kOffCtl + static_cast<int>(sizeof(Ctl));
 static_assert(kSmem <= 227 * 1024, "shared memory of one thread block");
 
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 256;  // two S tiles of 64 columns; O^T takes 64 columns a channel block from 0
+// O^T takes 64 columns a channel block from 0; two S tiles; two blocks of the
+// queries, two bf16 a column
+constexpr uint32_t kColS = 256, kColQ = 384;
 
 // fault codes: role in bits 8-11, barrier kind in bits 0-7
 enum : unsigned {
@@ -97,13 +111,15 @@ enum : unsigned {
   kFaultValue = 0xC01,
   kFaultSoftmax = 0xD01,
   kFaultToken = 0xE01,
+  kFaultQuery = 0xE03,
   kFaultTmem = 0xF02,  // TMEM does not begin at column 0
   kFaultSmem = 0xF01  // shared memory does not begin on a 1024-byte boundary
 };
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct AttnParams {
-  CUtensorMap tm_q;      // [rows][nh][d], boxes of [1][heads of a tile][64]
+  const __nv_bfloat16* q;
+  CUtensorMap tm_q;      // the queries [rows][nh][d], boxes of [1][heads of a tile][64]
   const char* cache;
   const int32_t* table;  // page table [rows, width] or index table [rows, width]
   const int32_t* lens;   // NULL: an index table
@@ -425,6 +441,17 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32])
       : "memory");
 }
 
+// 16 lanes x 32 columns, laid out over the warp alike.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
 // 16 columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -465,7 +492,8 @@ __device__ __forceinline__ bool any_softmax(bool x) {
 }
 
 template <bool E4M3>
-__global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(const __grid_constant__ AttnParams p) {
+  using C = Cfg<E4M3>;
   extern __shared__ __align__(1024) char smem[];
   const uint32_t base = ptx::smem_u32(smem);
   if (base & 1023u) {  // never: the declaration asks for it
@@ -479,15 +507,15 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
   const auto bar = [](uint64_t& b) { return ptx::smem_u32(&b); };
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(bar(ctl->full[s]), kLoadWarps<E4M3> * (E4M3 ? 33 : 32));
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(bar(ctl->full[s]), C::kLoadWarps * (E4M3 ? 33 : 32));
       ptx::mbar_init(bar(ctl->empty[s]), 1);
     }
     for (int i = 0; i < kSlotRing; ++i) {
       ptx::mbar_init(bar(ctl->slots_full[i]), 1);
-      ptx::mbar_init(bar(ctl->slots_empty[i]), kLoadWarps<E4M3>);
+      ptx::mbar_init(bar(ctl->slots_empty[i]), C::kLoadWarps);
     }
-    ptx::mbar_init(bar(ctl->q_full), 1);
+    ptx::mbar_init(bar(ctl->q_full), (C::kQueryBlocks > 0 ? 4 : 0) + (nblk > C::kQueryBlocks ? 1 : 0));
     ptx::mbar_init(bar(ctl->q_empty), 2);
     ptx::mbar_init(bar(ctl->drained[2]), 1);
     for (int k = 0; k < 2; ++k) {
@@ -506,7 +534,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
   }
   Walk w;
   int64_t total, nrun;
-  find_run<kThreads<E4M3>>(p, ctl, &w, &total, &nrun);
+  find_run<Cfg<E4M3>::kThreads>(p, ctl, &w, &total, &nrun);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -534,7 +562,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
         // the tile's mask was written before its stages were filled; they are
         // still full (only this tile's weights let them go)
         const uint32_t n0 = g * nblk;
-        wait_bar(bar(ctl->full[n0 % kStages]), (n0 / kStages) & 1, abort_flag, kFaultSoftmax);
+        wait_bar(bar(ctl->full[n0 % C::kStages]), (n0 / C::kStages) & 1, abort_flag, kFaultSoftmax);
         ptx::tc_fence_after();
         uint32_t r[32];
         tmem_ld_16x64(tmem + kColS + (g & 1) * 64 + lanes, r);
@@ -692,17 +720,16 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
     }
     if (!begun && tid == 0 && p.split) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);
   } else if (warp < kValueWarp) {
-    // ---------------------------------------------------------------- queries, S
-    // The whole warp walks, and every branch around the products is on a vote:
-    // what the compiler can prove uniform stays in uniform registers, where an
-    // MMA takes its operands from (a lone thread, or loops on a lane's own
-    // counts, took 60-130 cycles an MMA to move them there, against 33 and 49 of
-    // the tensor core for S and O^T).
+    // ---------------------------------------------------------------- S
+    // The whole warp walks, every branch around the products is on a vote, TMEM
+    // columns are constants and no call comes between: so operands stay in
+    // uniform registers, where an MMA takes them from (moving them there took
+    // 60-130 cycles an MMA, against 33 and 49 of the tensor core for S and O^T).
     const uint32_t id_s = ptx::idesc_bf16_f32(64, kTile, false, false);
     // operands' descriptors, to which address steps (in 16-byte units) are added
-    const uint64_t q_desc = ptx::smem_desc_sw128(base + kOffQ, 16, 1024);
-    const uint64_t c_desc = ptx::smem_desc_sw128(base + kOffRing, 16, 1024);
-    const int chunks = (p.l.d + 63) / 64;
+    const uint64_t q_desc = ptx::smem_desc_sw128(base + C::kOffQ, 16, 1024);
+    const uint64_t c_desc = ptx::smem_desc_sw128(base + C::kOffRing, 16, 1024);
+    const int chunks = (p.l.d - C::kQueryBlocks * kBlock + 63) / 64;
     const bool even = (p.l.d + 63) / 64 % 2 == 0;  // the last block has both its 64-channel halves
     const uint32_t mine = warp - kScoreWarp;  // tiles g with g % 2 == mine
     uint32_t g = 0, item = 0;
@@ -710,11 +737,11 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       if (!warp_any(x.j1 > x.j0)) continue;
       if (mine == 0) {
         if (item > 0) wait_bar_here(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultScore);
-        if (ptx::elect_one()) {
+        if (nblk > C::kQueryBlocks && ptx::elect_one()) {  // the channels that TMEM has no room for
           ptx::mbar_arrive_expect_tx(bar(ctl->q_full), chunks * p.tile_heads * 128);
           for (int c = 0; c < chunks; ++c)
-            ptx::tma_load_3d(base + kOffQ + c * 8192u, &p.tm_q, c * 64, x.head_tile * p.tile_heads,
-                             static_cast<int>(x.row), bar(ctl->q_full));
+            ptx::tma_load_3d(base + C::kOffQ + c * 8192u, &p.tm_q, C::kQueryBlocks * kBlock + c * 64,
+                             x.head_tile * p.tile_heads, static_cast<int>(x.row), bar(ctl->q_full));
         }
       }
       __syncwarp();
@@ -723,28 +750,36 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
         if ((g & 1) != mine) continue;
         if (g >= 2) wait_bar_here(bar(ctl->s_empty[g & 1]), ((g >> 1) - 1) & 1, abort_flag, kFaultScore);
         const uint32_t ds = kColS + mine * 64, n0 = g * nblk;
-        uint32_t s = n0 % kStages, phase = n0 / kStages & 1;
+        uint32_t s = n0 % C::kStages, phase = n0 / C::kStages & 1;
 #pragma unroll 1
         for (int b = 0; b < nblk; ++b) {
           wait_bar_here(bar(ctl->full[s]), phase, abort_flag, kFaultScore);
-          // The loading threads' stores and copies become visible to the tensor
-          // core by a fence on this side of the barrier: on theirs it would wait
-          // for their loads in flight, a memory latency a block.
           ptx::fence_proxy_async_smem();
           ptx::tc_fence_after();
-          const uint64_t qd = q_desc + b * (16384u >> 4), cd = c_desc + s * (kStageBytes >> 4);
-          const bool two = b < nblk - 1 || even;  // 64-channel halves, of four K steps
+          const uint64_t cd = c_desc + s * (kStageBytes >> 4);
+          const bool two = b < nblk - 1 || even;  // 64-channel halves
           if (ptx::elect_one()) {
+            if (b < C::kQueryBlocks) {
+              const uint32_t qt = kColQ + 64 * b;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ptx::tc_mma_ss(ds, qd + 2 * i, cd + 2 * i, id_s, i + b > 0);
-            if (two) {
+              for (int i = 0; i < 4; ++i) ptx::tc_mma_ts(ds, qt + 8 * i, cd + 2 * i, id_s, i + b > 0);
+              if (two) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                ptx::tc_mma_ss(ds, qd + (8192 >> 4) + 2 * i, cd + (kHalf >> 4) + 2 * i, id_s, 1);
+                for (int i = 0; i < 4; ++i) ptx::tc_mma_ts(ds, qt + 32 + 8 * i, cd + (kHalf >> 4) + 2 * i, id_s, 1);
+              }
+            } else {
+              const uint64_t qd = q_desc + (b - C::kQueryBlocks) * (16384 >> 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) ptx::tc_mma_ss(ds, qd + 2 * i, cd + 2 * i, id_s, i + b > 0);
+              if (two) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  ptx::tc_mma_ss(ds, qd + (8192 >> 4) + 2 * i, cd + (kHalf >> 4) + 2 * i, id_s, 1);
+              }
             }
           }
           __syncwarp();
-          if (++s == kStages) {
+          if (++s == C::kStages) {
             s = 0;
             phase ^= 1;
           }
@@ -757,7 +792,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       ++item;
     }
     // nothing may be in flight when the thread block leaves
-    if (item > 0) wait_bar_noabort(bar(ctl->q_full), (item - 1) & 1);
+    if (item > 0 && nblk > C::kQueryBlocks) wait_bar_noabort(bar(ctl->q_full), (item - 1) & 1);
     if (ptx::elect_one()) ptx::tc_commit(bar(ctl->drained[mine]));
     __syncwarp();
     wait_bar_noabort(bar(ctl->drained[mine]), 0);
@@ -765,7 +800,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
   } else if (warp == kValueWarp) {
     // ---------------------------------------------------------------- O^T += C^T P^T
     const uint32_t id_o = ptx::idesc_bf16_f32(128, p.tile_heads, true, false);
-    const uint64_t c_desc = ptx::smem_desc_sw128(base + kOffRing, kHalf, 1024);
+    const uint64_t c_desc = ptx::smem_desc_sw128(base + C::kOffRing, kHalf, 1024);
     const uint64_t p_desc = ptx::smem_desc_sw128(base + kOffP, 16, 1024);
     uint32_t g = 0, s = 0;
     while (warp_any(w.next(p, x))) {
@@ -775,18 +810,19 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_after();
         const uint64_t pd = p_desc + (g & 1) * (8192u >> 4);
+#pragma unroll 1
         for (int b = 0; b < nblk; ++b) {
           const uint64_t cd = c_desc + s * (kStageBytes >> 4);
           if (ptx::elect_one()) {
-            ptx::tc_mma_ss(tmem + b * 64, cd, pd, id_o, !first);
+            ptx::tc_mma_ss(b * 64, cd, pd, id_o, !first);
 #pragma unroll
             for (int k = 1; k < kTile / 16; ++k)
-              ptx::tc_mma_ss(tmem + b * 64, cd + k * (2048 >> 4), pd + k * (32 >> 4), id_o, 1);
+              ptx::tc_mma_ss(b * 64, cd + k * (2048 >> 4), pd + k * (32 >> 4), id_o, 1);
             ptx::tc_commit(bar(ctl->empty[s]));
             if (b == nblk - 1) ptx::tc_commit(bar(ctl->o_done[g & 1]));
           }
           __syncwarp();
-          if (++s == kStages) s = 0;
+          if (++s == C::kStages) s = 0;
         }
       }
     }
@@ -833,9 +869,54 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       marked = !live;  // behind the last tile, the mark that there is none
       live = more;
     }
+  } else if (!E4M3 && warp < C::kLoadWarp) {
+    // ---------------------------------------------------------------- queries
+    // Head h of the tile lies in TMEM lane 32 (h / 16) + h % 16, as S's row will.
+    // Half of a row's channels are loaded ahead, while S of the row before runs.
+    const uint32_t lanes = static_cast<uint32_t>(warp - C::kQueryWarp) << 21;
+    const int h = 16 * (warp - C::kQueryWarp) + lane / 4;  // and h + 8
+    const int chunks = (min(p.l.d, C::kQueryBlocks * kBlock) + 63) / 64;
+    uint32_t item = 0;
+    while (w.next(p, x)) {
+      if (x.j1 == x.j0) continue;
+      const int h0 = x.head_tile * p.tile_heads, heads = min(p.tile_heads, p.nh - h0);
+      const __nv_bfloat16* q = p.q + (x.row * p.nh + h0 + h) * p.l.d + 4 * (lane & 3);
+      uint32_t r[2][16];
+      const auto load = [&](int c0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {  // 16 channels (u / 2) of head h + 8 (u % 2)
+            const int c = 64 * (c0 + i) + 16 * (u >> 1);
+            uint2 v = make_uint2(0u, 0u);
+            if (h + 8 * (u & 1) < heads && c + 4 * (lane & 3) < p.l.d && c0 + i < chunks)
+              v = __ldg(reinterpret_cast<const uint2*>(q + 8 * (u & 1) * p.l.d + c));
+            r[i][4 * (u >> 1) + 2 * (u & 1)] = v.x;
+            r[i][4 * (u >> 1) + 2 * (u & 1) + 1] = v.y;
+          }
+      };
+      const auto store = [&](int c0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (c0 + i < chunks) tmem_st_16x32(tmem + kColQ + 32 * (c0 + i) + lanes, r[i]);
+      };
+      load(0);
+      if (item > 0) wait_bar(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultQuery);
+      ptx::tc_fence_after();
+      store(0);
+      if (chunks > 2) {
+        load(2);
+        store(2);
+      }
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(ctl->q_full));
+      ++item;
+    }
   } else {
     // ---------------------------------------------------------------- cache rows
-    const int v = warp - kLoadWarp;
+    const int v = warp - C::kLoadWarp;
     uint32_t g = 0, s = 0, phase = 1;  // tiles looked up; stage, and the phase of `empty` that lets it be filled
     bool ok = true;
     // The slots of the next tile, read with `take`; false behind the last.
@@ -851,7 +932,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       return ok && some;
     };
     const auto next_stage = [&] {
-      if (++s == kStages) {
+      if (++s == C::kStages) {
         s = 0;
         phase ^= 1;
       }
@@ -868,7 +949,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
       })) {
         for (int b = 0; b < nblk; ++b) {
           if (!wait_stage()) break;
-          copy_block(p, slot, b, tok, lane, base + kOffRing + s * kStageBytes);
+          copy_block(p, slot, b, tok, lane, base + C::kOffRing + s * kStageBytes);
           copies_arrive(bar(ctl->full[s]));
           next_stage();
         }
@@ -890,7 +971,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
 #pragma unroll
         for (int b = 0; b < kMaxBlocks; ++b) {
           if (b >= nblk || !wait_stage()) break;
-          const uint32_t stage = base + kOffRing + s * kStageBytes;
+          const uint32_t stage = base + C::kOffRing + s * kStageBytes;
           if (b * kBlock + 16 * item < p.l.nope) store_codes(raw.v[b], raw.scales, b, item, tok, stage);
           // a lane's arrival 33 times, or once with one of each lane's copies
           const bool pe = (b + 1) * kBlock > p.l.nope;
@@ -919,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads<E4M3>, 1) latent_attn_kernel(const __
   __syncthreads();
   if (warp == kScoreWarp) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(ctl->tmem, kTmemCols);
+    ptx::tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -1141,7 +1222,7 @@ int attend(AttnParams& p, const void* q, void* workspace, size_t workspace_bytes
                       {p.lens, p.lens ? static_cast<size_t>(p.rows) * 4 : 0}};
   Range out[] = {{p.O, vec}, {p.lse, p.lse ? heads * 4 : 0}, {workspace, 0}};
   const auto clash = [&] {
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 2; ++i) {
       for (const Range& x : in)
         if (overlaps(out[i].at, out[i].bytes, x.at, x.bytes)) return true;
       for (int j = 0; j < i; ++j)
@@ -1163,13 +1244,14 @@ int attend(AttnParams& p, const void* q, void* workspace, size_t workspace_bytes
     p.part_ml = reinterpret_cast<float2*>(ws + n.ml_off);
     p.split = reinterpret_cast<int4*>(ws + n.split_off);
   }
+  p.q = static_cast<const __nv_bfloat16*>(q);
   p.head_tiles = n.head_tiles;
   p.tile_heads = n.tile_heads;
   if (!opt_in_smem(dev.device) || !query_map(&p.tm_q, q, p.rows, p.nh, p.l.d, n.tile_heads)) return INVROPE_ERR_CUDA;
   if (fmt == KV_LATENT_E4M3)
-    latent_attn_kernel<true><<<n.grid, kThreads<true>, kSmem, s>>>(p);
+    latent_attn_kernel<true><<<n.grid, Cfg<true>::kThreads, kSmem, s>>>(p);
   else
-    latent_attn_kernel<false><<<n.grid, kThreads<false>, kSmem, s>>>(p);
+    latent_attn_kernel<false><<<n.grid, Cfg<false>::kThreads, kSmem, s>>>(p);
   if ((st = check_launch()) != INVROPE_OK || n.bytes == 0) return st;
   // programmatic dependent launch: the join's launch is processed while the
   // attention drains; its blocks wait in-kernel for the partials
