@@ -11,6 +11,7 @@ fallback: if the library is not built, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -355,25 +356,39 @@ def kv_latent_empty(num_pages: int, page_size: int, nope: int, pe: int, fmt: int
     return torch.empty(num_pages, page_size, nbytes // 2, dtype=torch.bfloat16, device=device)
 
 
+def _is(t, dtype, ndim):
+    return t.dtype is dtype and t.dim() == ndim and t.is_cuda and t.is_contiguous()
+
+
+@functools.lru_cache(maxsize=64)
+def _row_width(nope, pe, fmt):
+    return kv_latent_row_bytes(nope, pe, fmt) // (1 if fmt == KV_LATENT_E4M3 else 2)
+
+
 def _cache(cache, nope, pe):
     """Check a cache tensor against the channel split; returns its format. The
     dtype tells it: bf16 rows are the values, uint8 rows the e4m3 layout."""
     if not isinstance(cache, torch.Tensor):
         raise TypeError("cache must be a torch.Tensor")
-    if cache.dtype == torch.bfloat16:
-        fmt, width = KV_LATENT_BF16, nope + pe
-    else:
-        fmt, width = KV_LATENT_E4M3, kv_latent_row_bytes(nope, pe, KV_LATENT_E4M3)
-    _need(cache, "cache", torch.uint8 if fmt == KV_LATENT_E4M3 else torch.bfloat16, 3)
+    fmt = KV_LATENT_BF16 if cache.dtype is torch.bfloat16 else KV_LATENT_E4M3
+    dtype = torch.uint8 if fmt == KV_LATENT_E4M3 else torch.bfloat16
+    if not _is(cache, dtype, 3):
+        _need(cache, "cache", dtype, 3)
+    width = _row_width(nope, pe, fmt)
     if width and cache.shape[2] != width:  # width 0: the library says why the split is refused
         raise ValueError(f"cache rows must be {width} wide for nope={nope}, pe={pe}, got {cache.shape[2]}")
     return fmt
 
 
-def _same_device(device, **tensors):
+def _same_device(index, **tensors):
     for name, t in tensors.items():
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+
+
+def _raw_stream(index, stream):
+    """The stream's handle; the current stream's where none is given."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def kv_latent_write(cache, x, slots, nope: int, pe: int, stream=None):
@@ -381,14 +396,18 @@ def kv_latent_write(cache, x, slots, nope: int, pe: int, stream=None):
     ``slots`` [n] (slot = page * page_size + place in the page), quantising them
     where the cache is 8-bit; slots out of range store nothing. Returns ``cache``."""
     fmt = _cache(cache, nope, pe)
-    _need(x, "x", torch.bfloat16, 2)
-    _need(slots, "slots", torch.int32, 1)
-    n = x.shape[0]
-    if x.shape[1] != nope + pe or slots.shape[0] != n:
+    if not (isinstance(x, torch.Tensor) and _is(x, torch.bfloat16, 2)):
+        _need(x, "x", torch.bfloat16, 2)
+    if not (isinstance(slots, torch.Tensor) and _is(slots, torch.int32, 1)):
+        _need(slots, "slots", torch.int32, 1)
+    n, d = x.shape
+    if d != nope + pe or slots.shape[0] != n:
         raise ValueError(f"x must be [n, {nope + pe}] and slots [n]")
-    _same_device(cache.device, x=x, slots=slots)
-    st = lib().kv_latent_write(x.data_ptr(), slots.data_ptr(), cache.data_ptr(), n, cache.shape[0] * cache.shape[1],
-                               nope, pe, fmt, _stream_handle(cache.device, stream))
+    index = cache.get_device()
+    _same_device(index, x=x, slots=slots)
+    pages, size, _ = cache.shape
+    st = lib().kv_latent_write(x.data_ptr(), slots.data_ptr(), cache.data_ptr(), n, pages * size, nope, pe, fmt,
+                               _raw_stream(index, stream))
     _check(st, "kv_latent_write")
     return cache
 
@@ -397,17 +416,20 @@ def kv_latent_read(cache, slots, nope: int, pe: int, out=None, stream=None):
     """The bf16 vectors [n, nope+pe] that the cache holds at int32 ``slots`` [n]
     (zeros for a slot out of range)."""
     fmt = _cache(cache, nope, pe)
-    _need(slots, "slots", torch.int32, 1)
+    if not (isinstance(slots, torch.Tensor) and _is(slots, torch.int32, 1)):
+        _need(slots, "slots", torch.int32, 1)
     n = slots.shape[0]
+    index = cache.get_device()
     if out is None:
         out = _empty((n, nope + pe), torch.bfloat16, cache.device, stream)
     else:
         _need(out, "out", torch.bfloat16, 2)
         if tuple(out.shape) != (n, nope + pe):
             raise ValueError(f"out must be [{n}, {nope + pe}]")
-    _same_device(cache.device, slots=slots, out=out)
-    st = lib().kv_latent_read(cache.data_ptr(), slots.data_ptr(), out.data_ptr(), n, cache.shape[0] * cache.shape[1],
-                              nope, pe, fmt, _stream_handle(cache.device, stream))
+    _same_device(index, slots=slots, out=out)
+    pages, size, _ = cache.shape
+    st = lib().kv_latent_read(cache.data_ptr(), slots.data_ptr(), out.data_ptr(), n, pages * size, nope, pe, fmt,
+                              _raw_stream(index, stream))
     _check(st, "kv_latent_read")
     return out
 
@@ -417,35 +439,47 @@ def latent_attn_workspace_bytes(rows: int, nh: int, max_tokens: int, nope: int, 
     return int(lib().latent_attn_workspace_bytes(int(rows), int(nh), int(max_tokens), int(nope), int(pe)))
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(index, rows, nh, max_tokens, nope, pe):
+    with torch.cuda.device(index):  # the query goes by the current device's size
+        return latent_attn_workspace_bytes(rows, nh, max_tokens, nope, pe)
+
+
 def _attn_io(q, cache, nope, pe, max_tokens, O, lse, workspace, stream, **tables):
     """Checks and outputs common to the two attention calls."""
     fmt = _cache(cache, nope, pe)
-    _need(q, "q", torch.bfloat16, 3)
+    if not (isinstance(q, torch.Tensor) and _is(q, torch.bfloat16, 3)):
+        _need(q, "q", torch.bfloat16, 3)
     rows, nh, d = q.shape
     if d != nope + pe:
         raise ValueError(f"q must be [rows, nh, {nope + pe}]")
+    index, device = q.get_device(), q.device
     if O is None:
-        O = _empty(q.shape, torch.bfloat16, q.device, stream)
+        O = _empty((rows, nh, d), torch.bfloat16, device, stream)
     else:
         _need(O, "O", torch.bfloat16, 3)
         if O.shape != q.shape:
             raise ValueError("O must have q's shape")
+        tables["O"] = O
     if lse is None:
-        lse = _empty((rows, nh), torch.float32, q.device, stream)
+        lse = _empty((rows, nh), torch.float32, device, stream)
     else:
         _need(lse, "lse", torch.float32, 2)
         if tuple(lse.shape) != (rows, nh):
             raise ValueError(f"lse must be [{rows}, {nh}]")
+        tables["lse"] = lse
     if workspace is None:
-        nbytes = lib().latent_attn_workspace_bytes(rows, nh, max_tokens, nope, pe)
-        workspace = _empty((nbytes,), torch.uint8, q.device, stream) if nbytes else None
+        nbytes = _workspace_bytes(index, rows, nh, max_tokens, nope, pe)
+        if nbytes:
+            workspace = _empty((nbytes,), torch.uint8, device, stream)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     else:
         tables["workspace"] = workspace
-    _same_device(q.device, cache=cache, O=O, lse=lse, **tables)
-    ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    return fmt, O, lse, ws, workspace
+        nbytes = workspace.numel() * workspace.element_size()
+    _same_device(index, cache=cache, **tables)
+    return fmt, O, lse, (workspace.data_ptr() if workspace is not None else None), nbytes, workspace, \
+        _raw_stream(index, stream)
 
 
 def latent_attn_decode(q, cache, page_table, lens, nope: int, pe: int, scale=None, O=None, lse=None,
@@ -455,18 +489,19 @@ def latent_attn_decode(q, cache, page_table, lens, nope: int, pe: int, scale=Non
     ``page_table`` int32 [rows, max_pages], ``lens`` int32 [rows] tokens a row.
     ``scale`` defaults to ``(nope+pe) ** -0.5``. Returns ``(O bf16, lse fp32 [rows, nh])``;
     a row with nothing to attend to gives zeros and -inf."""
-    _need(page_table, "page_table", torch.int32, 2)
-    _need(lens, "lens", torch.int32, 1)
+    for t, name, ndim in ((page_table, "page_table", 2), (lens, "lens", 1)):
+        if not (isinstance(t, torch.Tensor) and _is(t, torch.int32, ndim)):
+            _need(t, name, torch.int32, ndim)
     max_pages = page_table.shape[1]
-    fmt, O, lse, ws, workspace = _attn_io(q, cache, nope, pe, max_pages * cache.shape[1], O, lse, workspace,
-                                          stream, page_table=page_table, lens=lens)
+    fmt, O, lse, ws, ws_bytes, workspace, handle = _attn_io(
+        q, cache, nope, pe, max_pages * cache.shape[1], O, lse, workspace, stream, page_table=page_table, lens=lens)
     rows, nh, d = q.shape
     if page_table.shape[0] != rows or lens.shape[0] != rows:
         raise ValueError(f"page_table must be [{rows}, max_pages] and lens [{rows}]")
-    handle = _stream_handle(q.device, stream)
+    pages, size, _ = cache.shape
     st = lib().latent_attn_decode(q.data_ptr(), cache.data_ptr(), page_table.data_ptr(), lens.data_ptr(), O.data_ptr(),
-                                  lse.data_ptr(), ws[0], ws[1], rows, nh, nope, pe, fmt, cache.shape[0],
-                                  cache.shape[1], max_pages, d ** -0.5 if scale is None else float(scale), handle)
+                                  lse.data_ptr(), ws, ws_bytes, rows, nh, nope, pe, fmt, pages, size, max_pages,
+                                  d ** -0.5 if scale is None else float(scale), handle)
     _check(st, "latent_attn_decode")
     return O, lse
 
@@ -475,15 +510,16 @@ def latent_attn_sparse(q, cache, idx, nope: int, pe: int, scale=None, O=None, ls
     """The same attention over the cache slots that ``idx`` int32 [rows, topk]
     selects for each row (the flat-global table of :func:`kv_idx_local_to_global`;
     entries out of range, such as -1 padding, are left out)."""
-    _need(idx, "idx", torch.int32, 2)
+    if not (isinstance(idx, torch.Tensor) and _is(idx, torch.int32, 2)):
+        _need(idx, "idx", torch.int32, 2)
     rows, topk = idx.shape
-    fmt, O, lse, ws, workspace = _attn_io(q, cache, nope, pe, topk, O, lse, workspace, stream, idx=idx)
+    fmt, O, lse, ws, ws_bytes, workspace, handle = _attn_io(q, cache, nope, pe, topk, O, lse, workspace, stream, idx=idx)
     if q.shape[0] != rows:
         raise ValueError("idx must have a row for each of q's")
     nh, d = q.shape[1:]
-    handle = _stream_handle(q.device, stream)
-    st = lib().latent_attn_sparse(q.data_ptr(), cache.data_ptr(), idx.data_ptr(), O.data_ptr(), lse.data_ptr(), ws[0],
-                                  ws[1], rows, nh, nope, pe, fmt, cache.shape[0] * cache.shape[1], topk,
+    pages, size, _ = cache.shape
+    st = lib().latent_attn_sparse(q.data_ptr(), cache.data_ptr(), idx.data_ptr(), O.data_ptr(), lse.data_ptr(), ws,
+                                  ws_bytes, rows, nh, nope, pe, fmt, pages * size, topk,
                                   d ** -0.5 if scale is None else float(scale), handle)
     _check(st, "latent_attn_sparse")
     return O, lse
