@@ -1,9 +1,10 @@
 // Writing the paged latent cache and reading it back (include/latent_attn.h).
 //
-// Both are one pass: a thread holds 8 channels of one token (16 bytes of bf16),
-// so the 8 threads of a 64-channel group sit in one warp and find the group's
-// largest magnitude with three shuffles; codes, scales and pe channels leave
-// in the same pass.
+// Both are one pass, bound by memory: a thread holds 16 channels of a token (an
+// "item"), a warp one token of 512 channels, and each thread kRows tokens at a
+// time, whose loads are all in flight before the first is used. The 4 threads of
+// a 64-channel group find its largest magnitude with two shuffles; codes, scales
+// and pe channels leave in the same pass.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -17,6 +18,7 @@ namespace {
 using latent::RowLayout;
 
 constexpr int kThreads = 256;
+constexpr int kRows = 4;
 
 // The scale's exponent: the least e with amax <= 448 * 2^e, kept to [kEMin, kEMax].
 // amax = m * 2^k with 1 <= m < 2 and 448 = 1.75 * 2^8, so e = k - 8, or k - 7
@@ -28,98 +30,113 @@ __device__ __forceinline__ int scale_exponent(float amax) {
   return min(max(e, latent::kEMin), latent::kEMax);
 }
 
+// `shift`: log2 of the threads a token has, a power of two >= ceil(d / 16), at
+// least the 4 of a group.
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads)
-    latent_write_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ slots, char* __restrict__ cache,
-                        int64_t n, int64_t num_slots, RowLayout l) {
-  const int units = l.d / 8;                 // 16-byte units of a token
-  const int padded = (units + 7) / 8 * 8;    // whole groups of 8 threads
-  const int64_t total = n * padded;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads; base < total; base += step) {
-    const int64_t g = base + threadIdx.x;
-    const int64_t i = g / padded;
-    const int u = static_cast<int>(g - i * padded);
-    const bool live = g < total && u < units;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    int64_t slot = -1;
-    if (live) {
-      v = __ldcs(x + i * units + u);
-      slot = slots[i];
-    }
-    const bool ok = live && slot >= 0 && slot < num_slots;
-    char* row = cache + (ok ? slot : 0) * static_cast<int64_t>(l.row_bytes);
-    if (!E4M3) {
-      if (ok) *reinterpret_cast<uint4*>(row + u * 16) = v;
-      continue;
-    }
-    const int c = u * 8;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float f[8], amax = 0.f;
-    bool finite = true;
+    latent_write_kernel(const char* __restrict__ x, const int32_t* __restrict__ slots, char* __restrict__ cache,
+                        int64_t n, int64_t num_slots, RowLayout l, int shift) {
+  const int c = 16 * (threadIdx.x & ((1 << shift) - 1));
+  const int per = kThreads >> shift;  // tokens a block takes side by side
+  const bool one = c < l.d, two = c + 8 < l.d;
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * per * kRows + (threadIdx.x >> shift);
+       i0 - (threadIdx.x >> shift) < n; i0 += static_cast<int64_t>(gridDim.x) * per * kRows) {
+    uint4 v[kRows][2];
+    int slot[kRows];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = ptx::bf16_lo_f32(w[k]);
-      f[2 * k + 1] = ptx::bf16_hi_f32(w[k]);
-      finite = finite && (w[k] & 0x7F80u) != 0x7F80u && (w[k] & 0x7F800000u) != 0x7F800000u;
-      amax = fmaxf(amax, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t i = i0 + r * per;
+      const bool live = i < n;
+      const char* row = x + i * (2 * l.d) + 2 * c;
+      v[r][0] = live && one ? __ldcs(reinterpret_cast<const uint4*>(row)) : make_uint4(0u, 0u, 0u, 0u);
+      v[r][1] = live && two ? __ldcs(reinterpret_cast<const uint4*>(row) + 1) : make_uint4(0u, 0u, 0u, 0u);
+      slot[r] = live ? __ldg(slots + i) : -1;
     }
-    if (!live || c >= l.nope) {  // a pe unit beside the last group's codes
-      amax = 0.f;
-      finite = true;
-    }
-    if (!finite) amax = __uint_as_float(0x7F800000u);
 #pragma unroll
-    for (int s = 1; s < 8; s *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, s));
-    if (!ok) continue;
-    if (c >= l.nope) {
-      *reinterpret_cast<uint4*>(row + l.nope + 2 * (c - l.nope)) = v;
-      continue;
-    }
-    const bool bad = __float_as_uint(amax) == 0x7F800000u;
-    const int e = bad ? 0 : scale_exponent(amax);
-    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e
-    uint32_t code[4];
+    for (int r = 0; r < kRows; ++r) {
+      const bool ok = one && slot[r] >= 0 && slot[r] < num_slots;
+      char* row = cache + static_cast<int64_t>(ok ? slot[r] : 0) * l.row_bytes;
+      if (!E4M3 || c >= l.nope) {
+        if (ok) {
+          uint4* to = reinterpret_cast<uint4*>(E4M3 ? row + l.nope + 2 * (c - l.nope) : row + 2 * c);
+          to[0] = v[r][0];
+          if (two) to[1] = v[r][1];
+        }
+      }
+      if (!E4M3) continue;
+      const uint32_t w[8] = {v[r][0].x, v[r][0].y, v[r][0].z, v[r][0].w, v[r][1].x, v[r][1].y, v[r][1].z, v[r][1].w};
+      float amax = 0.f;
+      bool finite = true;
+      if (c < l.nope) {  // nope is a multiple of 16: all codes or none
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      code[k] = bad ? 0u
-                    : __nv_cvt_float2_to_fp8x2(make_float2(f[2 * k] * inv, f[2 * k + 1] * inv), __NV_SATFINITE,
-                                               __NV_E4M3);
-    *reinterpret_cast<uint2*>(row + c) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
-    if (c % latent::kGroup == 0)
-      reinterpret_cast<unsigned char*>(row)[l.scale_off + c / latent::kGroup] =
-          static_cast<unsigned char>(bad ? 255 : e + 127);
+        for (int k = 0; k < 8; ++k) {
+          finite = finite && (w[k] & 0x7F80u) != 0x7F80u && (w[k] & 0x7F800000u) != 0x7F800000u;
+          amax = fmaxf(amax, fmaxf(fabsf(ptx::bf16_lo_f32(w[k])), fabsf(ptx::bf16_hi_f32(w[k]))));
+        }
+        if (!finite) amax = __uint_as_float(0x7F800000u);
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      if (!ok || c >= l.nope) continue;
+      const bool bad = __float_as_uint(amax) == 0x7F800000u;
+      const int e = bad ? 0 : scale_exponent(amax);
+      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e
+      uint32_t code[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        code[k] = bad ? 0u
+                      : __nv_cvt_float2_to_fp8x2(
+                            make_float2(ptx::bf16_lo_f32(w[k]) * inv, ptx::bf16_hi_f32(w[k]) * inv), __NV_SATFINITE,
+                            __NV_E4M3);
+      *reinterpret_cast<uint4*>(row + c) = make_uint4(code[0] | code[1] << 16, code[2] | code[3] << 16,
+                                                      code[4] | code[5] << 16, code[6] | code[7] << 16);
+      if (c % latent::kGroup == 0)
+        reinterpret_cast<unsigned char*>(row)[l.scale_off + c / latent::kGroup] =
+            static_cast<unsigned char>(bad ? 255 : e + 127);
+    }
   }
 }
 
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads)
-    latent_read_kernel(const char* __restrict__ cache, const int32_t* __restrict__ slots, uint4* __restrict__ out,
-                       int64_t n, int64_t num_slots, RowLayout l) {
-  const int units = l.d / 8;
-  const int64_t total = n * units;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t g = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; g < total; g += step) {
-    const int64_t i = g / units;
-    const int u = static_cast<int>(g - i * units);
-    const int64_t slot = slots[i];
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (slot >= 0 && slot < num_slots) {
-      const char* row = cache + slot * static_cast<int64_t>(l.row_bytes);
-      const int c = u * 8;
-      if (!E4M3) {
-        v = __ldg(reinterpret_cast<const uint4*>(row + u * 16));
-      } else if (c >= l.nope) {
-        v = __ldg(reinterpret_cast<const uint4*>(row + l.nope + 2 * (c - l.nope)));
-      } else {
-        const uint2 codes = __ldg(reinterpret_cast<const uint2*>(row + c));
-        const uint32_t s =
-            latent::scale_bf16x2(__ldg(reinterpret_cast<const unsigned char*>(row) + l.scale_off + c / latent::kGroup));
-        latent::e4m3x4_to_bf16(codes.x, s, v.x, v.y);
-        latent::e4m3x4_to_bf16(codes.y, s, v.z, v.w);
-      }
+    latent_read_kernel(const char* __restrict__ cache, const int32_t* __restrict__ slots, char* __restrict__ out,
+                       int64_t n, int64_t num_slots, RowLayout l, int shift) {
+  const int c = 16 * (threadIdx.x & ((1 << shift) - 1));
+  const int per = kThreads >> shift;
+  const bool one = c < l.d, two = c + 8 < l.d, codes = E4M3 && c < l.nope;
+  const int at = !E4M3 ? 2 * c : codes ? c : l.nope + 2 * (c - l.nope);
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * per * kRows + (threadIdx.x >> shift); i0 < n;
+       i0 += static_cast<int64_t>(gridDim.x) * per * kRows) {
+    int slot[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) slot[r] = i0 + r * per < n ? __ldg(slots + i0 + r * per) : -1;
+    uint4 v[kRows][2];
+    uint32_t byte[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const bool ok = one && slot[r] >= 0 && slot[r] < num_slots;
+      const char* row = cache + static_cast<int64_t>(ok ? slot[r] : 0) * l.row_bytes;
+      v[r][0] = ok ? __ldg(reinterpret_cast<const uint4*>(row + at)) : make_uint4(0u, 0u, 0u, 0u);
+      v[r][1] = ok && two && !codes ? __ldg(reinterpret_cast<const uint4*>(row + at) + 1) : make_uint4(0u, 0u, 0u, 0u);
+      byte[r] = ok && codes
+                    ? __ldg(reinterpret_cast<const unsigned char*>(row) + l.scale_off + c / latent::kGroup)
+                    : 127u;
     }
-    __stcs(out + g, v);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t i = i0 + r * per;
+      if (codes) {
+        const uint32_t s = latent::scale_bf16x2(byte[r]);
+        const uint4 w = v[r][0];
+        latent::e4m3x4_to_bf16(w.x, s, v[r][0].x, v[r][0].y);
+        latent::e4m3x4_to_bf16(w.y, s, v[r][0].z, v[r][0].w);
+        latent::e4m3x4_to_bf16(w.z, s, v[r][1].x, v[r][1].y);
+        latent::e4m3x4_to_bf16(w.w, s, v[r][1].z, v[r][1].w);
+      }
+      uint4* to = reinterpret_cast<uint4*>(out + i * (2 * l.d) + 2 * c);
+      if (one && i < n) __stcs(to, v[r][0]);
+      if (two && i < n) __stcs(to + 1, v[r][1]);
+    }
   }
 }
 
@@ -137,8 +154,16 @@ int check_rows(const void* vectors, const int32_t* slots, const void* cache, int
   return INVROPE_OK;
 }
 
-unsigned grid_for(int64_t threads, const DeviceInfo& dev) {
-  const int64_t blocks = (threads + kThreads - 1) / kThreads, most = static_cast<int64_t>(dev.sms) * 8;
+// log2 of the threads a token has.
+int threads_shift(const RowLayout& l) {
+  int shift = 2;
+  while ((16 << shift) < l.d) ++shift;
+  return shift;
+}
+
+unsigned grid_for(int64_t n, int shift, const DeviceInfo& dev) {
+  const int64_t each = static_cast<int64_t>(kThreads >> shift) * kRows;
+  const int64_t blocks = (n + each - 1) / each, most = static_cast<int64_t>(dev.sms) * 8;
   return static_cast<unsigned>(blocks < most ? blocks : most);
 }
 
@@ -165,13 +190,14 @@ extern "C" int kv_latent_write(const void* x, const int32_t* slots, void* cache,
   DeviceInfo dev;
   if ((st = current_device(&dev)) != INVROPE_OK) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = grid_for(n * ((l.d / 8 + 7) / 8 * 8), dev);
+  const int shift = threads_shift(l);
+  const unsigned grid = grid_for(n, shift, dev);
   if (fmt == KV_LATENT_E4M3)
-    latent_write_kernel<true><<<grid, kThreads, 0, s>>>(static_cast<const uint4*>(x), slots, static_cast<char*>(cache),
-                                                        n, num_slots, l);
+    latent_write_kernel<true><<<grid, kThreads, 0, s>>>(static_cast<const char*>(x), slots, static_cast<char*>(cache),
+                                                        n, num_slots, l, shift);
   else
-    latent_write_kernel<false><<<grid, kThreads, 0, s>>>(static_cast<const uint4*>(x), slots,
-                                                         static_cast<char*>(cache), n, num_slots, l);
+    latent_write_kernel<false><<<grid, kThreads, 0, s>>>(static_cast<const char*>(x), slots,
+                                                         static_cast<char*>(cache), n, num_slots, l, shift);
   return check_launch();
 }
 
@@ -188,12 +214,13 @@ extern "C" int kv_latent_read(const void* cache, const int32_t* slots, void* out
   DeviceInfo dev;
   if ((st = current_device(&dev)) != INVROPE_OK) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = grid_for(n * (l.d / 8), dev);
+  const int shift = threads_shift(l);
+  const unsigned grid = grid_for(n, shift, dev);
   if (fmt == KV_LATENT_E4M3)
     latent_read_kernel<true><<<grid, kThreads, 0, s>>>(static_cast<const char*>(cache), slots,
-                                                       static_cast<uint4*>(out), n, num_slots, l);
+                                                       static_cast<char*>(out), n, num_slots, l, shift);
   else
     latent_read_kernel<false><<<grid, kThreads, 0, s>>>(static_cast<const char*>(cache), slots,
-                                                        static_cast<uint4*>(out), n, num_slots, l);
+                                                        static_cast<char*>(out), n, num_slots, l, shift);
   return check_launch();
 }
