@@ -56,11 +56,18 @@ __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t byte) {
 // Four e4m3 codes -> four bf16 values. A code's exponent and mantissa bits,
 // moved into bf16's fields, read as value * 2^-120 (e4m3's bias is 7, bf16's
 // 127; e4m3 subnormals become bf16 subnormals); the product with `factor`, a
-// power of two twice, is exact.
+// power of two twice, is exact. Two codes are put in bytes 1 and 3, with byte 2
+// the copies of the first one's sign: one arithmetic shift by 4 then brings
+// both signs and fields to where bf16 has them, and one mask leaves just those.
+__device__ __forceinline__ uint32_t prmt_signs(uint32_t w, uint32_t selector) {  // 8 + n: byte n's sign, 8 times
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "r"(selector));
+  return r;
+}
 __device__ __forceinline__ void e4m3x4_times(uint32_t w, uint32_t factor, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0u, 0x1404u), b = __byte_perm(w, 0u, 0x3424u);
-  lo = mul_bf16x2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), factor);
-  hi = mul_bf16x2((b & 0x80008000u) | ((b >> 4) & 0x07F007F0u), factor);
+  const int a = static_cast<int>(prmt_signs(w, 0x1800u)), b = static_cast<int>(prmt_signs(w, 0x3A22u));
+  lo = mul_bf16x2(static_cast<uint32_t>(a >> 4) & 0x87F087F0u, factor);
+  hi = mul_bf16x2(static_cast<uint32_t>(b >> 4) & 0x87F087F0u, factor);
 }
 
 // The same times the group's scale: 2^120 and the scale, which together may
