@@ -64,8 +64,8 @@ constexpr int kScoreWarp = 4, kValueWarp = 6, kTokenWarp = 7;
 constexpr int kQueryChunk = 64 * 128;    // [64 heads][64 channels]
 template <bool E4M3>
 struct Cfg {
-  static constexpr int kQueryBlocks = E4M3 ? 0 : 2;  // 128-channel blocks of the queries in TMEM, two bf16 a column
-  static constexpr int kStages = E4M3 ? 9 : 11;      // a tile is up to 4
+  static constexpr int kQueryBlocks = 2;  // 128-channel blocks of the queries in TMEM, two bf16 a column
+  static constexpr int kStages = 11;      // a tile is up to 4
   static constexpr int kQueryWarp = 8;
   static constexpr int kLoadWarp = E4M3 ? 8 : 12;
   static constexpr int kLoadWarps = E4M3 ? 16 : 8;
@@ -337,82 +337,73 @@ __device__ __forceinline__ void copy_block(const AttnParams& p, const int (&slot
   }
 }
 
-// e4m3 rows: 4 tokens a warp, 8 lanes a token, 16 codes of every block a lane.
-// A tile's codes are in registers while in flight, two tiles at a time.
-// Lanes are laid out so that 8 in a row store 4 units each of two neighbouring
-// tokens: all 32 banks.
-struct RawTile {
-  uint4 v[kMaxBlocks];
-  uint2 scales;  // the row's scale bytes
-  int slot;      // this lane's token's, -1: left out
-};
+// e4m3 rows: half of the warps take even blocks, half odd ones, 8 lanes a token,
+// 16 codes a lane. The codes land in the stage itself, in the first of the two
+// units that the same lane will write their bf16 values to, and the token's
+// scales in the second unit of its first lane. (Loads to registers went through
+// what L1 has left beside 227 KB of shared memory, which held up every access of
+// the SM: 96 ragged rows took 305 us, and 220 without their loads.)
+constexpr int kCodeTokens = 2;  // tokens a lane has codes of
+constexpr int kCodeStep = kTile / kCodeTokens;
+constexpr uint32_t kCodesAhead = 2;  // blocks of a warp in flight
 
-__device__ __forceinline__ void load_16_if(uint4& v, const char* at, bool there) {  // 0 where it is not
-  v = make_uint4(0u, 0u, 0u, 0u);
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-      : "l"(at), "r"(static_cast<int>(there)));
-}
-
-__device__ __forceinline__ void load_codes(const AttnParams& p, RawTile& raw, int nblk, int item) {
-  const bool there = raw.slot >= 0;
-  const char* row = p.cache + static_cast<int64_t>(there ? raw.slot : 0) * p.l.row_bytes;
-  raw.scales = make_uint2(0u, 0u);
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %3, 0;\n\t"
-      "@p ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"  // rows end on a 16-byte boundary: 8 bytes are there
-      : "+r"(raw.scales.x), "+r"(raw.scales.y)
-      : "l"(row + p.l.scale_off), "r"(static_cast<int>(there)));
+__device__ __forceinline__ void copy_codes(const AttnParams& p, const int (&slot)[kCodeTokens], int b, int item,
+                                           uint32_t to) {
+  const int c = b * kBlock + 16 * item;
+  if (c >= p.l.nope) return;
 #pragma unroll
-  for (int b = 0; b < kMaxBlocks; ++b)
-    if (b < nblk) {
-      const int c = b * kBlock + 16 * item;
-      load_16_if(raw.v[b], row + c, there && c < p.l.nope);
-    }
+  for (int k = 0; k < kCodeTokens; ++k) {
+    const bool there = slot[k] >= 0;
+    const char* row = p.cache + static_cast<int64_t>(there ? slot[k] : 0) * p.l.row_bytes;
+    copy_16(to + k * kCodeStep * 128, row + c, there);
+    if (item == 0) copy_16((to + k * kCodeStep * 128) ^ 16u, row + p.l.scale_off, there);  // rows end on 16 bytes
+  }
 }
 
-// Block b's codes of this lane's token (token t of the tile) into the stage.
-__device__ __forceinline__ void store_codes(const uint4& w, const uint2& scales, int b, int item, int t,
-                                            uint32_t stage) {
-  const uint32_t two = (b & 2 ? scales.y : scales.x) >> (16 * (b & 1));
-  const uint32_t byte = (two >> (8 * (item >> 2))) & 255u;
+__device__ __forceinline__ uint4 load_16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t load_byte(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// 16 codes with the scale byte `byte` to the units at `to` and at to ^ 16.
+__device__ __forceinline__ void store_codes(const uint4& w, uint32_t byte, uint32_t to) {
   // 2^(byte - 127) times the 2^120 of the conversion is one bf16 factor up to a
-  // scale of 2^7; above, 2^127 is, and the rest of it another.
-  const bool over = byte > 134u && byte != 255u;
-  uint32_t f = byte == 255u ? 0x7FC0u : min(byte + 120u, 254u) << 7;
-  f |= f << 16;
+  // scale of 2^7; above, 2^127 is, and the rest of it (or NaN) another.
+  const uint32_t f = min(byte + 120u, 254u) * 0x00800080u;
   uint4 lo, hi;
   latent::e4m3x4_times(w.x, f, lo.x, lo.y);
   latent::e4m3x4_times(w.y, f, lo.z, lo.w);
   latent::e4m3x4_times(w.z, f, hi.x, hi.y);
   latent::e4m3x4_times(w.w, f, hi.z, hi.w);
-  if (over) {
-    const uint32_t r = latent::scale_bf16x2(byte - 7u);
+  if (byte > 134u) {
+    const uint32_t r = latent::scale_bf16x2(byte == 255u ? byte : byte - 7u);
     lo.x = latent::mul_bf16x2(lo.x, r), lo.y = latent::mul_bf16x2(lo.y, r);
     lo.z = latent::mul_bf16x2(lo.z, r), lo.w = latent::mul_bf16x2(lo.w, r);
     hi.x = latent::mul_bf16x2(hi.x, r), hi.y = latent::mul_bf16x2(hi.y, r);
     hi.z = latent::mul_bf16x2(hi.z, r), hi.w = latent::mul_bf16x2(hi.w, r);
   }
-  store_16(unit_addr(stage, t, 2 * item), lo);
-  store_16(unit_addr(stage, t, 2 * item + 1), hi);
+  store_16(to, lo);
+  store_16(to ^ 16u, hi);
 }
 
-// The pe channels of block b, and zeros behind the last channel, of tokens tok
-// and tok + 2: 16 lanes take a token's units of 8 channels.
-__device__ __forceinline__ void copy_pe(const AttnParams& p, const int (&slot)[2], int b, int tok, int lane,
+// The pe channels of block b, and zeros behind the last channel, of tokens tok,
+// tok + 2, tok + 32 and tok + 34: 16 lanes take a token's units of 8 channels.
+__device__ __forceinline__ void copy_pe(const AttnParams& p, const int (&slot)[2 * kCodeTokens], int b, int tok, int lane,
                                         uint32_t stage) {
   const int unit = lane & 15, c = b * kBlock + 8 * unit;
   if (c < p.l.nope) return;
   const char* from = p.cache + (c < p.l.d ? p.l.nope + 2 * (c - p.l.nope) : 0);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < 2 * kCodeTokens; ++k) {
     const bool there = slot[k] >= 0 && c < p.l.d;
-    copy_16(unit_addr(stage, tok + 2 * k, unit), from + static_cast<int64_t>(there ? slot[k] : 0) * p.l.row_bytes,
-            there);
+    copy_16(unit_addr(stage, tok + 2 * (k & 1) + kCodeStep * (k >> 1), unit),
+            from + static_cast<int64_t>(there ? slot[k] : 0) * p.l.row_bytes, there);
   }
 }
 
@@ -477,6 +468,48 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 // A condition that is the same on all lanes, as one the compiler knows to be.
 __device__ __forceinline__ bool warp_any(bool x) { return __any_sync(0xFFFFFFFFu, x); }
 
+// The first `channels` channels of a piece's queries into TMEM, by four warps:
+// head h of the tile in lane 32 (h / 16) + h % 16, as S's row will be. `ready`
+// waits for the products with the queries before, half of the loads in flight.
+template <typename Ready>
+__device__ __forceinline__ void put_queries(const AttnParams& p, const Piece& x, int channels, int quarter, int lane,
+                                            uint32_t to, Ready ready) {
+  const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
+  const int h = 16 * quarter + lane / 4;  // and h + 8
+  const int chunks = (min(p.l.d, channels) + 63) / 64;
+  const int h0 = x.head_tile * p.tile_heads, heads = min(p.tile_heads, p.nh - h0);
+  const __nv_bfloat16* q = p.q + (x.row * p.nh + h0 + h) * p.l.d + 4 * (lane & 3);
+  uint32_t r[2][16];
+  const auto load = [&](int c0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {  // 16 channels (u / 2) of head h + 8 (u % 2)
+        const int c = 64 * (c0 + i) + 16 * (u >> 1);
+        uint2 v = make_uint2(0u, 0u);
+        if (h + 8 * (u & 1) < heads && c + 4 * (lane & 3) < p.l.d && c0 + i < chunks)
+          v = __ldg(reinterpret_cast<const uint2*>(q + 8 * (u & 1) * p.l.d + c));
+        r[i][4 * (u >> 1) + 2 * (u & 1)] = v.x;
+        r[i][4 * (u >> 1) + 2 * (u & 1) + 1] = v.y;
+      }
+  };
+  const auto store = [&](int c0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (c0 + i < chunks) tmem_st_16x32(to + 32 * (c0 + i) + lanes, r[i]);
+  };
+  load(0);
+  ready();
+  store(0);
+  if (chunks > 2) {
+    load(2);
+    store(2);
+  }
+  ptx::tmem_st_wait();
+  ptx::tc_fence_before();
+  __syncwarp();
+}
+
 // True on all 128 softmax threads when it is on any of them; a barrier.
 __device__ __forceinline__ bool any_softmax(bool x) {
   uint32_t r;
@@ -508,7 +541,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      ptx::mbar_init(bar(ctl->full[s]), C::kLoadWarps * (E4M3 ? 33 : 32));
+      ptx::mbar_init(bar(ctl->full[s]), E4M3 ? C::kLoadWarps / 2 : C::kLoadWarps * 32);
       ptx::mbar_init(bar(ctl->empty[s]), 1);
     }
     for (int i = 0; i < kSlotRing; ++i) {
@@ -557,6 +590,10 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
       const int h0 = x.head_tile * p.tile_heads;
       const int heads = min(p.tile_heads, p.nh - h0);
       float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+      if (E4M3 && x.j1 > x.j0) {  // (the products with the queries before are in)
+        put_queries(p, x, C::kQueryBlocks * kBlock, warp, lane, tmem + kColQ, [] {});
+        if (lane == 0) ptx::mbar_arrive(bar(ctl->q_full));
+      }
       for (int j = x.j0; j < x.j1; ++j, ++g) {
         wait_bar(bar(ctl->s_full[g & 1]), (g >> 1) & 1, abort_flag, kFaultSoftmax);
         // the tile's mask was written before its stages were filled; they are
@@ -871,46 +908,13 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
     }
   } else if (!E4M3 && warp < C::kLoadWarp) {
     // ---------------------------------------------------------------- queries
-    // Head h of the tile lies in TMEM lane 32 (h / 16) + h % 16, as S's row will.
-    // Half of a row's channels are loaded ahead, while S of the row before runs.
-    const uint32_t lanes = static_cast<uint32_t>(warp - C::kQueryWarp) << 21;
-    const int h = 16 * (warp - C::kQueryWarp) + lane / 4;  // and h + 8
-    const int chunks = (min(p.l.d, C::kQueryBlocks * kBlock) + 63) / 64;
     uint32_t item = 0;
     while (w.next(p, x)) {
       if (x.j1 == x.j0) continue;
-      const int h0 = x.head_tile * p.tile_heads, heads = min(p.tile_heads, p.nh - h0);
-      const __nv_bfloat16* q = p.q + (x.row * p.nh + h0 + h) * p.l.d + 4 * (lane & 3);
-      uint32_t r[2][16];
-      const auto load = [&](int c0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {  // 16 channels (u / 2) of head h + 8 (u % 2)
-            const int c = 64 * (c0 + i) + 16 * (u >> 1);
-            uint2 v = make_uint2(0u, 0u);
-            if (h + 8 * (u & 1) < heads && c + 4 * (lane & 3) < p.l.d && c0 + i < chunks)
-              v = __ldg(reinterpret_cast<const uint2*>(q + 8 * (u & 1) * p.l.d + c));
-            r[i][4 * (u >> 1) + 2 * (u & 1)] = v.x;
-            r[i][4 * (u >> 1) + 2 * (u & 1) + 1] = v.y;
-          }
-      };
-      const auto store = [&](int c0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (c0 + i < chunks) tmem_st_16x32(tmem + kColQ + 32 * (c0 + i) + lanes, r[i]);
-      };
-      load(0);
-      if (item > 0) wait_bar(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultQuery);
-      ptx::tc_fence_after();
-      store(0);
-      if (chunks > 2) {
-        load(2);
-        store(2);
-      }
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before();
-      __syncwarp();
+      put_queries(p, x, C::kQueryBlocks * kBlock, warp - C::kQueryWarp, lane, tmem + kColQ, [&] {
+        if (item > 0) wait_bar(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultQuery);
+        ptx::tc_fence_after();
+      });
       if (lane == 0) ptx::mbar_arrive(bar(ctl->q_full));
       ++item;
     }
@@ -956,40 +960,85 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
         if (!ok) break;
       }
     } else {
-      const int tok = 4 * v + 2 * (lane >> 4) + (lane >> 2 & 1), item = (lane >> 1 & 4) | (lane & 3);
-      RawTile one, two;
-      const auto load = [&](RawTile& raw) {
-        const bool live = next_slots([&](const int* slots) { raw.slot = slots[tok]; });
-        if (live) load_codes(p, raw, nblk, item);
-        return live;
-      };
-      const auto convert = [&](const RawTile& raw) {
-        // the slots of tokens 4 v + lane / 16 and that + 2 for the pe copies
-        int pe_slot[2];
+      const int odd = v & 1, tok = 4 * (v >> 1) + 2 * (lane >> 4) + (lane >> 2 & 1);
+      const int item = (lane >> 1 & 4) | (lane & 3);
+      const uint32_t off = unit_addr(0, tok, 2 * item), scale = unit_addr(0, tok, 1) + (item >> 2);
+      const int mine = (nblk - odd + 1) / 2;  // blocks of a tile that are this warp's
+      int slot[kCodeTokens];
+      int next = mine, oldest = 0;      // of a tile's blocks: the next to be copied, the oldest in flight
+      uint32_t tile = 0, s_out = 0, pending = 0;
+      bool more = true;
+      for (;;) {
+        while (more && pending < kCodesAhead) {
+          if (next == mine) {
+            if (tile++ > 0) {
+              s += nblk;
+              if (s >= C::kStages) {
+                s -= C::kStages;
+                phase ^= 1;
+              }
+            }
+            more = next_slots([&](const int* slots) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) pe_slot[k] = __shfl_sync(0xFFFFFFFFu, raw.slot, 16 * k + 4 * (lane >> 4));
-#pragma unroll
-        for (int b = 0; b < kMaxBlocks; ++b) {
-          if (b >= nblk || !wait_stage()) break;
-          const uint32_t stage = base + C::kOffRing + s * kStageBytes;
-          if (b * kBlock + 16 * item < p.l.nope) store_codes(raw.v[b], raw.scales, b, item, tok, stage);
-          // a lane's arrival 33 times, or once with one of each lane's copies
-          const bool pe = (b + 1) * kBlock > p.l.nope;
-          if (pe) {
-            copy_pe(p, pe_slot, b, 4 * v + (lane >> 4), lane, stage);
-            copies_arrive(bar(ctl->full[s]));
+              for (int k = 0; k < kCodeTokens; ++k) slot[k] = slots[tok + kCodeStep * k];
+            });
+            next = 0;
+            continue;
           }
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_n(bar(ctl->full[s]), pe ? 1 : 33);
-          next_stage();
+          const int b = 2 * next + odd;
+          const bool wrap = s + b >= C::kStages;
+          const uint32_t at = wrap ? s + b - C::kStages : s + b, ph = wrap ? phase ^ 1 : phase;
+          if (pending > 0) {  // if it is not free yet, the blocks in flight come first
+            if (!__all_sync(0xFFFFFFFFu, ptx::mbar_test_wait(bar(ctl->empty[at]), ph))) break;
+          } else {
+            ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(ctl->empty[at]), ph, abort_flag, kFaultLoad));
+            if (!ok) break;
+          }
+          const uint32_t stage = base + C::kOffRing + at * kStageBytes;
+          copy_codes(p, slot, b, item, stage + off);
+          if ((b + 1) * kBlock > p.l.nope) {
+            int pe_slot[2 * kCodeTokens];
+#pragma unroll
+            for (int k = 0; k < 2 * kCodeTokens; ++k)
+              pe_slot[k] = __shfl_sync(0xFFFFFFFFu, slot[k >> 1], 16 * (k & 1) + 4 * (lane >> 4));
+            copy_pe(p, pe_slot, b, 4 * (v >> 1) + (lane >> 4), lane, stage);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          ++next;
+          ++pending;
         }
-        return ok;
-      };
-      bool live1 = load(one), live2 = live1 && load(two);
-      while (live1 && convert(one)) {
-        live1 = live2 && load(one);
-        if (!live2 || !convert(two)) break;
-        live2 = live1 && load(two);
+        if (!ok || pending == 0) break;
+        if (pending == 1)
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();  // the scales are another lane's copy
+        const int b = 2 * oldest + odd;
+        const uint32_t at = s_out + b >= C::kStages ? s_out + b - C::kStages : s_out + b;
+        const uint32_t to = base + C::kOffRing + at * kStageBytes;
+        if (b * kBlock < p.l.nope) {
+          const bool codes = b * kBlock + 16 * item < p.l.nope;
+          uint4 w[kCodeTokens];
+          uint32_t byte[kCodeTokens];
+#pragma unroll
+          for (int k = 0; k < kCodeTokens; ++k) {
+            w[k] = load_16(to + off + k * kCodeStep * 128);
+            byte[k] = load_byte(to + scale + k * kCodeStep * 128 + 2 * b);
+          }
+          __syncwarp();  // all have read them
+          if (codes) {
+#pragma unroll
+            for (int k = 0; k < kCodeTokens; ++k) store_codes(w[k], byte[k], to + off + k * kCodeStep * 128);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(ctl->full[at]));
+        --pending;
+        if (++oldest == mine) {
+          oldest = 0;
+          s_out += nblk;
+          if (s_out >= C::kStages) s_out -= C::kStages;
+        }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // nothing lands after the block has left
