@@ -16,18 +16,32 @@
 // over several blocks leaves one partial (accumulators, reference and sum in
 // fp32) for each, which latent_join_kernel adds up in a fixed order.
 //
-// bf16 rows go straight to shared memory (cp.async: boxes of 128 bytes by row
-// went no faster than 4.4 TB/s through TMA, 16 bytes a thread 6.6); 256 channels
-// of the queries then lie in TMEM, which leaves the ring nearly three tiles (two
-// let a tile's loads begin when the one two before was done: 5% slower). e4m3 rows
-// are held in registers while in flight and converted on the way, by more warps,
-// which leaves no registers for that.
+// Rows reach shared memory by cp.async, 16 bytes a thread (6.6 TB/s on pages of
+// 64 rows of 1 KB; boxes of 64 rows x 128 bytes through TMA went no faster than
+// 4.4). e4m3 codes land in the stage that they are converted in (copy_codes). 256
+// channels of the queries lie in TMEM, which leaves the ring nearly three tiles:
+// with two, a tile's loads began when the one two before was done (5% slower).
 //
 // Warps: 0-3 softmax and output (TMEM lanes), 4 S of even tiles, 5 S of odd tiles
 // (one issues while the other waits, so that the tensor core does not), 6 O^T
 // (either product goes out as soon as what it needs is there: a late tile does not
-// hold up the one that frees its stages), 7 the tokens' slots, then with bf16 rows
-// 4 for the queries in TMEM, and those that load rows.
+// hold up the one that frees its stages), 7 the tokens' slots, then 8 that load
+// bf16 rows after 4 that bring queries to TMEM, or 16 that load e4m3 rows (there
+// the softmax warps bring the queries: 28 warps would have 72 registers each).
+//
+// Bound: a tile of 64 tokens x 512 channels takes the tensor core 1840 cycles (32
+// MMAs of 33 cycles for S, M = 64 being half its rate, 16 of 49 for O^T, whose
+// operands shared memory delivers in 48) and DRAM, at 6.8 TB/s over 152 SMs, 2800
+// cycles with bf16 rows and 1650 with e4m3. Measured, alone on the GPU:
+//   bf16, 2048 rows of 2048 tokens (L2 hits): 641 us, 858 TFLOP/s, 2900 cycles a
+//     tile. What is left beside the products is a stage's way round: load, S,
+//     softmax (1500 cycles from S to the weights) and O^T take about 8000 cycles,
+//     of which the ring covers 11/4 tiles.
+//   bf16, 32 rows of 1 to 16384 tokens: 67.6 us, 4.0 TB/s with start and join, 6.2
+//     in between.
+//   e4m3, 96 rows of 1 to 24000 tokens: 281 us, 2.5 TB/s, 540 TFLOP/s; 4500 cycles
+//     a tile. Conversion in place makes a stage's way round longer by 64 KB of
+//     shared-memory writes a tile, beside the 229 KB that the MMAs read.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -55,34 +69,30 @@ constexpr int kMaxBlocks = latent::kMaxD / kBlock;
 constexpr int kStageBytes = kTile * kBlock * 2;
 constexpr int kHalf = kTile * 128;       // one 64-channel half of a stage
 constexpr int kSlotRing = 4;     // tiles whose slots are looked up ahead of their loads
-constexpr int kMaskRing = 32;    // tiles whose token masks are kept: those of both rings, at most 14
+constexpr int kMaskRing = 32;    // tiles whose token masks are kept: those of both rings and of the loading warps, at most 17
 constexpr int kOverhead = 2;     // what a row costs beside its tiles, in tiles
 constexpr int kMinUnits = 4;     // units of the line a thread block takes at least
 
 constexpr int kSoftmaxThreads = 128;
 constexpr int kScoreWarp = 4, kValueWarp = 6, kTokenWarp = 7;
 constexpr int kQueryChunk = 64 * 128;    // [64 heads][64 channels]
+constexpr int kQueryBlocks = 2;  // 128-channel blocks of the queries in TMEM, two bf16 a column
+constexpr int kStages = 11;      // a tile is up to 4
 template <bool E4M3>
 struct Cfg {
-  static constexpr int kQueryBlocks = 2;  // 128-channel blocks of the queries in TMEM, two bf16 a column
-  static constexpr int kStages = 11;      // a tile is up to 4
   static constexpr int kQueryWarp = 8;
   static constexpr int kLoadWarp = E4M3 ? 8 : 12;
   static constexpr int kLoadWarps = E4M3 ? 16 : 8;
   static constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
-  // shared memory, from a 1024-byte boundary: the other blocks of the queries,
-  // the ring (stages of 2 x [64 tokens][64 channels])
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffRing = (kMaxBlocks - kQueryBlocks) * 2 * kQueryChunk;
-  static constexpr int kEnd = kOffRing + kStages * kStageBytes;
 };
-constexpr int kMaxStages = Cfg<false>::kStages;
 constexpr int kMaxWarps = Cfg<true>::kThreads / 32;
-static_assert(Cfg<false>::kEnd == Cfg<true>::kEnd, "both fill the same shared memory");
-constexpr int kOffP = Cfg<false>::kEnd;                     // 2 x [64 heads][64 tokens]
+// shared memory, from a 1024-byte boundary: the other blocks of the queries, the
+// ring (stages of 2 x [64 tokens][64 channels]), weights, barriers and tables
+constexpr int kOffRing = (kMaxBlocks - kQueryBlocks) * 2 * kQueryChunk;
+constexpr int kOffP = kOffRing + kStages * kStageBytes;  // 2 x [64 heads][64 tokens]
 constexpr int kOffCtl = kOffP + 2 * 64 * 128;
 struct Ctl {
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t full[kStages], empty[kStages];
   uint64_t slots_full[kSlotRing], slots_empty[kSlotRing];
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], drained[3];
   uint64_t mask[kMaskRing];     // bit t: token t of the tile is attended to
@@ -319,10 +329,10 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Every loading warp takes a few tokens of every block, so that a stage that
-// comes free is full again after the work of those few: with a block to a warp
-// its 32 copies, or 8 to 16 conversions, lay between any stage's release and
-// its next use (1100 and 2800-3500 cycles of a 6500-cycle loop).
+// All loading warps (of e4m3 rows, every other one) take a few tokens of a block,
+// so that a stage that comes free is full again after the work of those few: with
+// a block to a warp its 32 copies, or 8 to 16 conversions, lay between any stage's
+// release and its next use (1100 and 2800-3500 cycles of a 6500-cycle loop).
 
 // bf16 rows: 8 tokens a warp, two an instruction (16 lanes a token's 256 bytes).
 __device__ __forceinline__ void copy_block(const AttnParams& p, const int (&slot)[4], int b, int tok, int lane,
@@ -341,8 +351,11 @@ __device__ __forceinline__ void copy_block(const AttnParams& p, const int (&slot
 // 16 codes a lane. The codes land in the stage itself, in the first of the two
 // units that the same lane will write their bf16 values to, and the token's
 // scales in the second unit of its first lane. (Loads to registers went through
-// what L1 has left beside 227 KB of shared memory, which held up every access of
-// the SM: 96 ragged rows took 305 us, and 220 without their loads.)
+// what L1 has left beside 227 KB of shared memory, and with it full every access
+// of the SM waited: 96 ragged rows took 305 us whatever was in flight, and 220
+// without their loads.) Two blocks in flight a warp: one took 325 us, three, which
+// hold stages for longer, 300; 8 warps of twice the tokens 299, and 16 that take 4
+// tokens of every block 377.
 constexpr int kCodeTokens = 2;  // tokens a lane has codes of
 constexpr int kCodeStep = kTile / kCodeTokens;
 constexpr uint32_t kCodesAhead = 2;  // blocks of a warp in flight
@@ -540,7 +553,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
   const auto bar = [](uint64_t& b) { return ptx::smem_u32(&b); };
 
   if (tid == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(bar(ctl->full[s]), E4M3 ? C::kLoadWarps / 2 : C::kLoadWarps * 32);
       ptx::mbar_init(bar(ctl->empty[s]), 1);
     }
@@ -548,7 +561,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
       ptx::mbar_init(bar(ctl->slots_full[i]), 1);
       ptx::mbar_init(bar(ctl->slots_empty[i]), C::kLoadWarps);
     }
-    ptx::mbar_init(bar(ctl->q_full), (C::kQueryBlocks > 0 ? 4 : 0) + (nblk > C::kQueryBlocks ? 1 : 0));
+    ptx::mbar_init(bar(ctl->q_full), 4 + (nblk > kQueryBlocks ? 1 : 0));
     ptx::mbar_init(bar(ctl->q_empty), 2);
     ptx::mbar_init(bar(ctl->drained[2]), 1);
     for (int k = 0; k < 2; ++k) {
@@ -567,7 +580,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
   }
   Walk w;
   int64_t total, nrun;
-  find_run<Cfg<E4M3>::kThreads>(p, ctl, &w, &total, &nrun);
+  find_run<C::kThreads>(p, ctl, &w, &total, &nrun);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -591,7 +604,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
       const int heads = min(p.tile_heads, p.nh - h0);
       float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
       if (E4M3 && x.j1 > x.j0) {  // (the products with the queries before are in)
-        put_queries(p, x, C::kQueryBlocks * kBlock, warp, lane, tmem + kColQ, [] {});
+        put_queries(p, x, kQueryBlocks * kBlock, warp, lane, tmem + kColQ, [] {});
         if (lane == 0) ptx::mbar_arrive(bar(ctl->q_full));
       }
       for (int j = x.j0; j < x.j1; ++j, ++g) {
@@ -599,7 +612,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
         // the tile's mask was written before its stages were filled; they are
         // still full (only this tile's weights let them go)
         const uint32_t n0 = g * nblk;
-        wait_bar(bar(ctl->full[n0 % C::kStages]), (n0 / C::kStages) & 1, abort_flag, kFaultSoftmax);
+        wait_bar(bar(ctl->full[n0 % kStages]), (n0 / kStages) & 1, abort_flag, kFaultSoftmax);
         ptx::tc_fence_after();
         uint32_t r[32];
         tmem_ld_16x64(tmem + kColS + (g & 1) * 64 + lanes, r);
@@ -764,9 +777,9 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
     // 60-130 cycles an MMA, against 33 and 49 of the tensor core for S and O^T).
     const uint32_t id_s = ptx::idesc_bf16_f32(64, kTile, false, false);
     // operands' descriptors, to which address steps (in 16-byte units) are added
-    const uint64_t q_desc = ptx::smem_desc_sw128(base + C::kOffQ, 16, 1024);
-    const uint64_t c_desc = ptx::smem_desc_sw128(base + C::kOffRing, 16, 1024);
-    const int chunks = (p.l.d - C::kQueryBlocks * kBlock + 63) / 64;
+    const uint64_t q_desc = ptx::smem_desc_sw128(base, 16, 1024);
+    const uint64_t c_desc = ptx::smem_desc_sw128(base + kOffRing, 16, 1024);
+    const int chunks = (p.l.d - kQueryBlocks * kBlock + 63) / 64;
     const bool even = (p.l.d + 63) / 64 % 2 == 0;  // the last block has both its 64-channel halves
     const uint32_t mine = warp - kScoreWarp;  // tiles g with g % 2 == mine
     uint32_t g = 0, item = 0;
@@ -774,10 +787,10 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
       if (!warp_any(x.j1 > x.j0)) continue;
       if (mine == 0) {
         if (item > 0) wait_bar_here(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultScore);
-        if (nblk > C::kQueryBlocks && ptx::elect_one()) {  // the channels that TMEM has no room for
+        if (nblk > kQueryBlocks && ptx::elect_one()) {  // the channels that TMEM has no room for
           ptx::mbar_arrive_expect_tx(bar(ctl->q_full), chunks * p.tile_heads * 128);
           for (int c = 0; c < chunks; ++c)
-            ptx::tma_load_3d(base + C::kOffQ + c * 8192u, &p.tm_q, C::kQueryBlocks * kBlock + c * 64,
+            ptx::tma_load_3d(base + c * 8192u, &p.tm_q, kQueryBlocks * kBlock + c * 64,
                              x.head_tile * p.tile_heads, static_cast<int>(x.row), bar(ctl->q_full));
         }
       }
@@ -787,7 +800,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
         if ((g & 1) != mine) continue;
         if (g >= 2) wait_bar_here(bar(ctl->s_empty[g & 1]), ((g >> 1) - 1) & 1, abort_flag, kFaultScore);
         const uint32_t ds = kColS + mine * 64, n0 = g * nblk;
-        uint32_t s = n0 % C::kStages, phase = n0 / C::kStages & 1;
+        uint32_t s = n0 % kStages, phase = n0 / kStages & 1;
 #pragma unroll 1
         for (int b = 0; b < nblk; ++b) {
           wait_bar_here(bar(ctl->full[s]), phase, abort_flag, kFaultScore);
@@ -796,7 +809,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
           const uint64_t cd = c_desc + s * (kStageBytes >> 4);
           const bool two = b < nblk - 1 || even;  // 64-channel halves
           if (ptx::elect_one()) {
-            if (b < C::kQueryBlocks) {
+            if (b < kQueryBlocks) {
               const uint32_t qt = kColQ + 64 * b;
 #pragma unroll
               for (int i = 0; i < 4; ++i) ptx::tc_mma_ts(ds, qt + 8 * i, cd + 2 * i, id_s, i + b > 0);
@@ -805,7 +818,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
                 for (int i = 0; i < 4; ++i) ptx::tc_mma_ts(ds, qt + 32 + 8 * i, cd + (kHalf >> 4) + 2 * i, id_s, 1);
               }
             } else {
-              const uint64_t qd = q_desc + (b - C::kQueryBlocks) * (16384 >> 4);
+              const uint64_t qd = q_desc + (b - kQueryBlocks) * (16384 >> 4);
 #pragma unroll
               for (int i = 0; i < 4; ++i) ptx::tc_mma_ss(ds, qd + 2 * i, cd + 2 * i, id_s, i + b > 0);
               if (two) {
@@ -816,7 +829,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
             }
           }
           __syncwarp();
-          if (++s == C::kStages) {
+          if (++s == kStages) {
             s = 0;
             phase ^= 1;
           }
@@ -829,7 +842,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
       ++item;
     }
     // nothing may be in flight when the thread block leaves
-    if (item > 0 && nblk > C::kQueryBlocks) wait_bar_noabort(bar(ctl->q_full), (item - 1) & 1);
+    if (item > 0 && nblk > kQueryBlocks) wait_bar_noabort(bar(ctl->q_full), (item - 1) & 1);
     if (ptx::elect_one()) ptx::tc_commit(bar(ctl->drained[mine]));
     __syncwarp();
     wait_bar_noabort(bar(ctl->drained[mine]), 0);
@@ -837,7 +850,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
   } else if (warp == kValueWarp) {
     // ---------------------------------------------------------------- O^T += C^T P^T
     const uint32_t id_o = ptx::idesc_bf16_f32(128, p.tile_heads, true, false);
-    const uint64_t c_desc = ptx::smem_desc_sw128(base + C::kOffRing, kHalf, 1024);
+    const uint64_t c_desc = ptx::smem_desc_sw128(base + kOffRing, kHalf, 1024);
     const uint64_t p_desc = ptx::smem_desc_sw128(base + kOffP, 16, 1024);
     uint32_t g = 0, s = 0;
     while (warp_any(w.next(p, x))) {
@@ -859,7 +872,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
             if (b == nblk - 1) ptx::tc_commit(bar(ctl->o_done[g & 1]));
           }
           __syncwarp();
-          if (++s == C::kStages) s = 0;
+          if (++s == kStages) s = 0;
         }
       }
     }
@@ -911,7 +924,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
     uint32_t item = 0;
     while (w.next(p, x)) {
       if (x.j1 == x.j0) continue;
-      put_queries(p, x, C::kQueryBlocks * kBlock, warp - C::kQueryWarp, lane, tmem + kColQ, [&] {
+      put_queries(p, x, kQueryBlocks * kBlock, warp - C::kQueryWarp, lane, tmem + kColQ, [&] {
         if (item > 0) wait_bar(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultQuery);
         ptx::tc_fence_after();
       });
@@ -936,7 +949,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
       return ok && some;
     };
     const auto next_stage = [&] {
-      if (++s == C::kStages) {
+      if (++s == kStages) {
         s = 0;
         phase ^= 1;
       }
@@ -953,7 +966,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
       })) {
         for (int b = 0; b < nblk; ++b) {
           if (!wait_stage()) break;
-          copy_block(p, slot, b, tok, lane, base + C::kOffRing + s * kStageBytes);
+          copy_block(p, slot, b, tok, lane, base + kOffRing + s * kStageBytes);
           copies_arrive(bar(ctl->full[s]));
           next_stage();
         }
@@ -973,8 +986,8 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
           if (next == mine) {
             if (tile++ > 0) {
               s += nblk;
-              if (s >= C::kStages) {
-                s -= C::kStages;
+              if (s >= kStages) {
+                s -= kStages;
                 phase ^= 1;
               }
             }
@@ -986,15 +999,15 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
             continue;
           }
           const int b = 2 * next + odd;
-          const bool wrap = s + b >= C::kStages;
-          const uint32_t at = wrap ? s + b - C::kStages : s + b, ph = wrap ? phase ^ 1 : phase;
+          const bool wrap = s + b >= kStages;
+          const uint32_t at = wrap ? s + b - kStages : s + b, ph = wrap ? phase ^ 1 : phase;
           if (pending > 0) {  // if it is not free yet, the blocks in flight come first
             if (!__all_sync(0xFFFFFFFFu, ptx::mbar_test_wait(bar(ctl->empty[at]), ph))) break;
           } else {
             ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(ctl->empty[at]), ph, abort_flag, kFaultLoad));
             if (!ok) break;
           }
-          const uint32_t stage = base + C::kOffRing + at * kStageBytes;
+          const uint32_t stage = base + kOffRing + at * kStageBytes;
           copy_codes(p, slot, b, item, stage + off);
           if ((b + 1) * kBlock > p.l.nope) {
             int pe_slot[2 * kCodeTokens];
@@ -1014,8 +1027,8 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
           asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();  // the scales are another lane's copy
         const int b = 2 * oldest + odd;
-        const uint32_t at = s_out + b >= C::kStages ? s_out + b - C::kStages : s_out + b;
-        const uint32_t to = base + C::kOffRing + at * kStageBytes;
+        const uint32_t at = s_out + b >= kStages ? s_out + b - kStages : s_out + b;
+        const uint32_t to = base + kOffRing + at * kStageBytes;
         if (b * kBlock < p.l.nope) {
           const bool codes = b * kBlock + 16 * item < p.l.nope;
           uint4 w[kCodeTokens];
@@ -1037,7 +1050,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
         if (++oldest == mine) {
           oldest = 0;
           s_out += nblk;
-          if (s_out >= C::kStages) s_out -= C::kStages;
+          if (s_out >= kStages) s_out -= kStages;
         }
       }
     }

@@ -123,6 +123,33 @@ def test_decode_many_short_rows():
     _decode_case(lens, 5, 48, 16, 8, BF16, seed=3)
 
 
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+@pytest.mark.parametrize("nope,pe", [(48, 16), (128, 64), (320, 64), (448, 64)])
+def test_decode_ragged_rows_of_every_block_count(fmt, nope, pe):
+    """One to four blocks of 128 channels a tile: the ring's stages, and which
+    warps fill them, fall differently on the tiles."""
+    lens = [int(n) for n in np.random.default_rng(nope).integers(0, 400, 350)]
+    _decode_case(lens, 9, nope, pe, 16, fmt, seed=nope)
+
+
+def test_groups_whose_scales_lie_far_apart():
+    """Scales above 2^7 need two factors on the way to bf16; the queries are zero
+    in the channels of large values, so that only the output shows them."""
+    nope, pe, n, nh = 448, 64, 500, 20
+    d, size = nope + pe, torch.ones(nope + pe)
+    for group, e in enumerate([0, 20, 60, 100, -60, 8, 40]):
+        size[64 * group:64 * group + 64] = 2.0 ** e
+    x = (torch.randn(n, d, generator=torch.Generator().manual_seed(5)) * size).to(torch.bfloat16).cuda()
+    cache = ir.kv_latent_empty(n, 1, nope, pe, E4M3)
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    ir.kv_latent_write(cache, x, slots, nope, pe)
+    values = f64(ir.kv_latent_read(cache, slots, nope, pe))
+    assert (np.abs(values - f64(x)) <= np.abs(f64(x)) * 2.0 ** -4 + size.numpy() * 2.0 ** -8).all()
+    q = _q(3, nh, d, 6) * (size <= 1.0).to(torch.bfloat16).cuda()
+    O, lse = ir.latent_attn_sparse(q, cache, slots[None].repeat(3, 1).contiguous(), nope, pe, d ** -0.5)
+    _check(q, values, lambda r: np.arange(n), d ** -0.5, O, lse)
+
+
 @pytest.mark.parametrize("size,scale", [(1.0, 0.0), (30.0, None), (1.0, -0.3), (4.0, 2.0)])
 def test_decode_scales_and_peaked_rows(size, scale):
     """Zero and negative scales, and scores large enough that the running
