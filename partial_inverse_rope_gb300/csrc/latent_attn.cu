@@ -39,9 +39,10 @@
 //     of which the ring covers 11/4 tiles.
 //   bf16, 32 rows of 1 to 16384 tokens: 67.6 us, 4.0 TB/s with start and join, 6.2
 //     in between.
-//   e4m3, 96 rows of 1 to 24000 tokens: 281 us, 2.5 TB/s, 540 TFLOP/s; 4500 cycles
-//     a tile. Conversion in place makes a stage's way round longer by 64 KB of
-//     shared-memory writes a tile, beside the 229 KB that the MMAs read.
+//   e4m3, 96 rows of 4000 to 20000 tokens: 272 us, 2.6 TB/s, 555 TFLOP/s; 4350
+//     cycles a tile, of which shared memory is busy for 3600: 1540 for the MMAs'
+//     operands, 2050 for codes that land, are read and are written as bf16, and
+//     the rest. Issue slots are 56% busy.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -348,20 +349,22 @@ __device__ __forceinline__ void copy_block(const AttnParams& p, const int (&slot
 }
 
 // e4m3 rows: half of the warps take even blocks, half odd ones, 8 lanes a token,
-// 16 codes a lane. The codes land in the stage itself, in the first of the two
-// units that the same lane will write their bf16 values to, and the token's
-// scales in the second unit of its first lane. (Loads to registers went through
+// 16 codes a lane. The codes land in the stage itself, in the token's own units,
+// and the token's scales behind them: in a block of codes alone in their order,
+// else, where the pe channels lie already, each in the first of the two units that
+// its lane will write the bf16 values to (everywhere so, 32 bytes of a row came
+// apart in two: 281 against 272 us). (Loads to registers went through
 // what L1 has left beside 227 KB of shared memory, and with it full every access
 // of the SM waited: 96 ragged rows took 305 us whatever was in flight, and 220
-// without their loads.) Two blocks in flight a warp: one took 325 us, three, which
-// hold stages for longer, 300; 8 warps of twice the tokens 299, and 16 that take 4
-// tokens of every block 377.
+// without their loads.) Two blocks in flight a warp: with 281 us for that, one took
+// 325 and three, which hold stages for longer, 300; 8 warps of twice the tokens
+// 299, and 16 that take 4 tokens of every block 377.
 constexpr int kCodeTokens = 2;  // tokens a lane has codes of
 constexpr int kCodeStep = kTile / kCodeTokens;
 constexpr uint32_t kCodesAhead = 2;  // blocks of a warp in flight
 
 __device__ __forceinline__ void copy_codes(const AttnParams& p, const int (&slot)[kCodeTokens], int b, int item,
-                                           uint32_t to) {
+                                           uint32_t to, uint32_t scales) {
   const int c = b * kBlock + 16 * item;
   if (c >= p.l.nope) return;
 #pragma unroll
@@ -369,7 +372,7 @@ __device__ __forceinline__ void copy_codes(const AttnParams& p, const int (&slot
     const bool there = slot[k] >= 0;
     const char* row = p.cache + static_cast<int64_t>(there ? slot[k] : 0) * p.l.row_bytes;
     copy_16(to + k * kCodeStep * 128, row + c, there);
-    if (item == 0) copy_16((to + k * kCodeStep * 128) ^ 16u, row + p.l.scale_off, there);  // rows end on 16 bytes
+    if (item == 0) copy_16(scales + k * kCodeStep * 128, row + p.l.scale_off, there);  // rows end on 16 bytes
   }
 }
 
@@ -975,7 +978,12 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
     } else {
       const int odd = v & 1, tok = 4 * (v >> 1) + 2 * (lane >> 4) + (lane >> 2 & 1);
       const int item = (lane >> 1 & 4) | (lane & 3);
-      const uint32_t off = unit_addr(0, tok, 2 * item), scale = unit_addr(0, tok, 1) + (item >> 2);
+      const uint32_t off = unit_addr(0, tok, 2 * item);
+      // where codes and scales land: in a block of codes alone, in order
+      const auto land = [&](int b) { return (b + 1) * kBlock > p.l.nope ? off : tok * 128 + ((item ^ (tok & 1) << 2) << 4); };
+      const auto land_scales = [&](int b) {
+        return (b + 1) * kBlock > p.l.nope ? unit_addr(0, tok, 1) : kHalf + tok * 128 + ((tok & 7) << 4);
+      };
       const int mine = (nblk - odd + 1) / 2;  // blocks of a tile that are this warp's
       int slot[kCodeTokens];
       int next = mine, oldest = 0;      // of a tile's blocks: the next to be copied, the oldest in flight
@@ -1008,7 +1016,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
             if (!ok) break;
           }
           const uint32_t stage = base + kOffRing + at * kStageBytes;
-          copy_codes(p, slot, b, item, stage + off);
+          copy_codes(p, slot, b, item, stage + land(b), stage + land_scales(b));
           if ((b + 1) * kBlock > p.l.nope) {
             int pe_slot[2 * kCodeTokens];
 #pragma unroll
@@ -1035,8 +1043,8 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
           uint32_t byte[kCodeTokens];
 #pragma unroll
           for (int k = 0; k < kCodeTokens; ++k) {
-            w[k] = load_16(to + off + k * kCodeStep * 128);
-            byte[k] = load_byte(to + scale + k * kCodeStep * 128 + 2 * b);
+            w[k] = load_16(to + land(b) + k * kCodeStep * 128);
+            byte[k] = load_byte(to + land_scales(b) + k * kCodeStep * 128 + 2 * b + (item >> 2));
           }
           __syncwarp();  // all have read them
           if (codes) {
