@@ -1078,9 +1078,10 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
 // tiles: O = sum_k w_k part_k / sum_k w_k sum_k, w_k = 2^(reference_k - the
 // largest). A warp takes a (row, head), 4 x 128 channels; with few of them (a
 // long row over many runs) a block takes 128 channels of one, a warp every
-// fourth partial. All reads of a step are in flight at once: the time is a few
-// L2 latencies (one block a head with its loads in turn took 20-40 us).
-constexpr int kJoinWarps = 4;
+// eighth partial. All reads of a step are in flight at once: the time is a few
+// L2 latencies, 8 us behind 32 ragged rows (one block a head with its loads in
+// turn took 20-40 us; weights computed beside the partials' loads 1 us more).
+constexpr int kJoinWarps = 8;
 constexpr int kMaxRuns = 256;
 
 struct JoinParams {
@@ -1092,10 +1093,11 @@ struct JoinParams {
   int runs, nh, tile_heads, d;
 };
 
-__global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(JoinParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps, 4) latent_join_kernel(JoinParams p) {
   __shared__ int4 todo[kMaxRuns];  // (pieces, row, head tile, first run) of the split rows
   __shared__ int count[kJoinWarps];
   __shared__ float4 sums[kJoinWarps][32];
+  __shared__ float weight[kJoinWarps][kMaxRuns];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   ptx::griddep_wait();  // launched early: wait for the partials
   int n = 0;
@@ -1129,16 +1131,32 @@ __global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(JoinParams
     const bool live = u < units && head < p.nh;
     const int pieces = live ? e.x : 0;
     const auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * e.w : 2 * (e.w + k) + 1) * p.tile_heads + h; };
-    float top = -INFINITY;
-    for (int k = lane; k < pieces; k += 32) top = fmaxf(top, p.part_ml[slot(k)].x);
+    float2 ml[kMaxRuns / 32];
+    float top = -INFINITY, sum = 0.f;
+    if (pieces <= 32) {
+      ml[0] = make_float2(-INFINITY, 0.f);
+      if (lane < pieces) ml[0] = __ldg(p.part_ml + slot(lane));
+      top = ml[0].x;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kMaxRuns / 32; ++i) {
+        ml[i] = make_float2(-INFINITY, 0.f);
+        if (lane + 32 * i < pieces) ml[i] = __ldg(p.part_ml + slot(lane + 32 * i));
+      }
+#pragma unroll
+      for (int i = 0; i < kMaxRuns / 32; ++i) top = fmaxf(top, ml[i].x);
+    }
     for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    for (int k = lane; k < pieces; k += 32) {
-      const float2 ml = p.part_ml[slot(k)];
-      sum += exp2_fast(ml.x - ref) * ml.y;
+#pragma unroll
+    for (int i = 0; i < kMaxRuns / 32; ++i) {
+      if (32 * i >= pieces) break;
+      const float w = exp2_fast(ml[i].x - ref);
+      sum += w * ml[i].y;
+      weight[warp][lane + 32 * i] = w;
     }
     for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    __syncwarp();
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t out = static_cast<int64_t>(e.y) * p.nh + head;
     // partials k0, k0 + step, ... of channels 128 q + 4 lane and on
@@ -1146,7 +1164,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(JoinParams
       const int c = 128 * q + 4 * lane;
 #pragma unroll 8
       for (int k = k0; k < pieces; k += step) {
-        const float w = exp2_fast(__ldg(&p.part_ml[slot(k)].x) - ref);
+        const float w = weight[warp][k];
         if (c < p.d) {
           const float4 v = __ldg(reinterpret_cast<const float4*>(p.part + slot(k) * p.d + c));
           acc.x += w * v.x;
@@ -1182,7 +1200,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(JoinParams
       float4 acc[kMaxBlocks] = {};
 #pragma unroll 4
       for (int k = 0; k < pieces; ++k) {
-        const float w = exp2_fast(__ldg(&p.part_ml[slot(k)].x) - ref);
+        const float w = weight[warp][k];
 #pragma unroll
         for (int q = 0; q < kMaxBlocks; ++q) {
           const int c = 128 * q + 4 * lane;
@@ -1199,6 +1217,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(JoinParams
       for (int q = 0; q < kMaxBlocks; ++q)
         if (q < q1) store(acc[q], q);
     }
+    __syncwarp();  // the weights are read
     if (live && p.lse && lane == 0 && q0 == 0 && (!wide || warp == 0))
       p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
   }
@@ -1327,7 +1346,7 @@ int attend(AttnParams& p, const void* q, void* workspace, size_t workspace_bytes
   // attention drains; its blocks wait in-kernel for the partials
   const JoinParams jp{p.part, p.part_ml, p.split, p.O, p.lse, n.grid, p.nh, n.tile_heads, p.l.d};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(dev.sms * 8));
+  cfg.gridDim = dim3(static_cast<unsigned>(dev.sms * 4));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
