@@ -1,10 +1,20 @@
 // Writing the paged latent cache and reading it back (include/latent_attn.h).
 //
-// Both are one pass, bound by memory: a thread holds 16 channels of a token (an
-// "item"), a warp one token of 512 channels, and each thread kRows tokens at a
-// time, whose loads are all in flight before the first is used. The 4 threads of
-// a 64-channel group find its largest magnitude with two shuffles; codes, scales
-// and pe channels leave in the same pass.
+// Both are one pass, bound by memory: a thread holds 16 channels of a token, a
+// warp one token of 512 channels, and each thread kRows tokens at a time, whose
+// loads are all in flight before the first is used. The 4 threads of a 64-channel
+// group find its largest magnitude with two shuffles; codes, scales and pe
+// channels leave in the same pass. Vectors go past the cache's lines (streaming
+// loads and stores): they are used once.
+//
+// Measured for rows of 448 + 64 channels: 65536 e4m3 rows are read back in 24.4 us
+// (106 MB, 4.35 TB/s; with 8 channels and one token a thread at a time 28.8), of
+// which launch and tail are 5; 16384 are written in 8.8 us and read in 9.3 on the
+// GPU alone, with the vectors out of DRAM. A few rows take 4-5 us, one round of
+// dependent reads (slot, row) and a launch.
+//
+// Rounding: a code is rounded once, to nearest even, from x * 2^-e, which is exact
+// in fp32; what is read back, code * 2^e, is exact in bf16.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
