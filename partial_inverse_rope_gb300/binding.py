@@ -513,7 +513,8 @@ def latent_attn_sparse(q, cache, idx, nope: int, pe: int, scale=None, O=None, ls
     if not (isinstance(idx, torch.Tensor) and _is(idx, torch.int32, 2)):
         _need(idx, "idx", torch.int32, 2)
     rows, topk = idx.shape
-    fmt, O, lse, ws, ws_bytes, workspace, handle = _attn_io(q, cache, nope, pe, topk, O, lse, workspace, stream, idx=idx)
+    fmt, O, lse, ws, ws_bytes, workspace, handle = _attn_io(
+        q, cache, nope, pe, topk, O, lse, workspace, stream, idx=idx)
     if q.shape[0] != rows:
         raise ValueError("idx must have a row for each of q's")
     nh, d = q.shape[1:]

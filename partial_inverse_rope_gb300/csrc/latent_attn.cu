@@ -33,16 +33,17 @@
 // MMAs of 33 cycles for S, M = 64 being half its rate, 16 of 49 for O^T, whose
 // operands shared memory delivers in 48) and DRAM, at 6.8 TB/s over 152 SMs, 2800
 // cycles with bf16 rows and 1650 with e4m3. Measured, alone on the GPU:
-//   bf16, 2048 rows of 2048 tokens (L2 hits): 641 us, 858 TFLOP/s, 2900 cycles a
-//     tile. What is left beside the products is a stage's way round: load, S,
-//     softmax (1500 cycles from S to the weights) and O^T take about 8000 cycles,
-//     of which the ring covers 11/4 tiles.
-//   bf16, 32 rows of 1 to 16384 tokens: 67.6 us, 4.0 TB/s with start and join, 6.2
+//   bf16, 2048 rows of 2048 tokens of 65536 (L2 hits): 641 us, 858 TFLOP/s, 2900
+//     cycles a tile; 596 us where they are of 64, 618 with nothing to load, so it is
+//     not the rows: shared memory delivers for 1540 cycles a tile to the MMAs and
+//     takes in and gives out the rest for 680, most of it beside O^T's, which use all
+//     that it delivers.
+//   bf16, 32 rows of 1 to 16384 tokens: 67.3 us, 4.05 TB/s with start and join, 6.2
 //     in between.
 //   e4m3, 96 rows of 4000 to 20000 tokens: 272 us, 2.6 TB/s, 555 TFLOP/s; 4350
 //     cycles a tile, of which shared memory is busy for 3600: 1540 for the MMAs'
 //     operands, 2050 for codes that land, are read and are written as bf16, and
-//     the rest. Issue slots are 56% busy.
+//     the rest. Issue slots are 59% busy.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -70,7 +71,7 @@ constexpr int kMaxBlocks = latent::kMaxD / kBlock;
 constexpr int kStageBytes = kTile * kBlock * 2;
 constexpr int kHalf = kTile * 128;       // one 64-channel half of a stage
 constexpr int kSlotRing = 4;     // tiles whose slots are looked up ahead of their loads
-constexpr int kMaskRing = 32;    // tiles whose token masks are kept: those of both rings and of the loading warps, at most 17
+constexpr int kMaskRing = 32;    // tiles whose token masks are kept: those of both rings and in between, at most 17
 constexpr int kOverhead = 2;     // what a row costs beside its tiles, in tiles
 constexpr int kMinUnits = 4;     // units of the line a thread block takes at least
 
@@ -378,7 +379,10 @@ __device__ __forceinline__ void copy_codes(const AttnParams& p, const int (&slot
 
 __device__ __forceinline__ uint4 load_16(uint32_t at) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t load_byte(uint32_t at) {
@@ -410,8 +414,8 @@ __device__ __forceinline__ void store_codes(const uint4& w, uint32_t byte, uint3
 
 // The pe channels of block b, and zeros behind the last channel, of tokens tok,
 // tok + 2, tok + 32 and tok + 34: 16 lanes take a token's units of 8 channels.
-__device__ __forceinline__ void copy_pe(const AttnParams& p, const int (&slot)[2 * kCodeTokens], int b, int tok, int lane,
-                                        uint32_t stage) {
+__device__ __forceinline__ void copy_pe(const AttnParams& p, const int (&slot)[2 * kCodeTokens], int b, int tok,
+                                        int lane, uint32_t stage) {
   const int unit = lane & 15, c = b * kBlock + 8 * unit;
   if (c < p.l.nope) return;
   const char* from = p.cache + (c < p.l.d ? p.l.nope + 2 * (c - p.l.nope) : 0);
@@ -980,7 +984,9 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
       const int item = (lane >> 1 & 4) | (lane & 3);
       const uint32_t off = unit_addr(0, tok, 2 * item);
       // where codes and scales land: in a block of codes alone, in order
-      const auto land = [&](int b) { return (b + 1) * kBlock > p.l.nope ? off : tok * 128 + ((item ^ (tok & 1) << 2) << 4); };
+      const auto land = [&](int b) {
+        return (b + 1) * kBlock > p.l.nope ? off : tok * 128 + ((item ^ (tok & 1) << 2) << 4);
+      };
       const auto land_scales = [&](int b) {
         return (b + 1) * kBlock > p.l.nope ? unit_addr(0, tok, 1) : kHalf + tok * 128 + ((tok & 7) << 4);
       };
@@ -1130,7 +1136,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) latent_join_kernel(JoinPar
     const int h = unit % p.tile_heads, head = e.z * p.tile_heads + h;
     const bool live = u < units && head < p.nh;
     const int pieces = live ? e.x : 0;
-    const auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * e.w : 2 * (e.w + k) + 1) * p.tile_heads + h; };
+    const auto slot = [&](int k) {
+      return static_cast<int64_t>(k == 0 ? 2 * e.w : 2 * (e.w + k) + 1) * p.tile_heads + h;
+    };
     float2 ml[kMaxRuns / 32];
     float top = -INFINITY, sum = 0.f;
     if (pieces <= 32) {

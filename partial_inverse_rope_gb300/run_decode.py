@@ -118,7 +118,8 @@ def main(argv=None):
     us = e0.elapsed_time(e1) * 1e3 / max(1, args.steps)
     fault = ir.invrope_take_device_fault()
     print(f"{args.rows} sequences of {int(server.lens.min())} to {int(server.lens.max())} tokens, {args.fmt} cache: "
-          f"{us:.1f} us a step{' (graph)' if args.graph else ''}; outputs finite: {finite}; watchdog fault code {fault}")
+          f"{us:.1f} us a step{' (graph)' if args.graph else ''}; outputs finite: {finite}; "
+          f"watchdog fault code {fault}")
     return 1 if fault or not finite else 0
 
 
