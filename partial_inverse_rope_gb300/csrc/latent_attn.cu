@@ -709,7 +709,9 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
         for (int i = 0; i < 2; ++i) {
           const int h = hq + 8 * i;
           if (whole) {
-            ctl->inv[h] = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+            // not for a row without tiles: no barrier of a tile lies between this
+            // and another warp's output of the row before, which reads inv
+            if (x.j1 > x.j0) ctl->inv[h] = sum[i] == 0.f ? 0.f : 1.f / sum[i];
             if (p.lse && h < heads)
               p.lse[out + h] = sum[i] == 0.f ? -INFINITY : (m[i] + log2f(sum[i])) * 0.6931471805599453f;
           } else if (h < heads) {
@@ -744,7 +746,8 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
             uint32_t o[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const float2 f = *reinterpret_cast<const float2*>(ctl->inv + h1 + 2 * k);
+              float2 f = make_float2(0.f, 0.f);
+              if (x.j1 > x.j0) f = *reinterpret_cast<const float2*>(ctl->inv + h1 + 2 * k);
               const float even_h = __uint_as_float(v[2 * k]) * f.x, odd_h = __uint_as_float(v[2 * k + 1]) * f.y;
               const float give = odd ? even_h : odd_h, keep = odd ? odd_h : even_h;
               const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);

@@ -132,6 +132,17 @@ def test_decode_ragged_rows_of_every_block_count(fmt, nope, pe):
     _decode_case(lens, 9, nope, pe, 16, fmt, seed=nope)
 
 
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+@pytest.mark.parametrize("nh,nope,pe", [(128, 272, 16), (64, 448, 64), (40, 96, 32)])
+def test_rows_between_empty_ones(fmt, nh, nope, pe):
+    """A row without tokens has no tile, and so none of a tile's barriers: it must
+    not touch what a slower warp still needs for the output of the row before."""
+    for seed in range(6):
+        rng = np.random.default_rng(seed)
+        lens = [int(n) for n in rng.choice([0, 1, 1, 70, 200], 400, p=[0.5, 0.2, 0.2, 0.05, 0.05])]
+        _decode_case(lens, nh, nope, pe, 8, fmt, seed=seed, size=0.2)
+
+
 def test_groups_whose_scales_lie_far_apart():
     """Scales above 2^7 need two factors on the way to bf16; the queries are zero
     in the channels of large values, so that only the output shows them."""
