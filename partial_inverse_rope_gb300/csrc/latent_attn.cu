@@ -606,13 +606,20 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // TMEM lane field, 32 * warp
     bool begun = false;  // a split row began in this block
     uint32_t g = 0;      // tiles so far
+    uint32_t item = 0;   // rows with tiles whose queries this warp has brought
     while (w.next(p, x)) {
       const int h0 = x.head_tile * p.tile_heads;
       const int heads = min(p.tile_heads, p.nh - h0);
       float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-      if (E4M3 && x.j1 > x.j0) {  // (the products with the queries before are in)
-        put_queries(p, x, kQueryBlocks * kBlock, warp, lane, tmem + kColQ, [] {});
+      if (E4M3 && x.j1 > x.j0) {
+        // (the products with the queries before are in; but a warp of S that had no
+        // tile of that row may not have looked at its phase of q_full yet)
+        put_queries(p, x, kQueryBlocks * kBlock, warp, lane, tmem + kColQ, [&] {
+          if (item > 0) wait_bar(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultQuery);
+          ptx::tc_fence_after();
+        });
         if (lane == 0) ptx::mbar_arrive(bar(ctl->q_full));
+        ++item;
       }
       for (int j = x.j0; j < x.j1; ++j, ++g) {
         wait_bar(bar(ctl->s_full[g & 1]), (g >> 1) & 1, abort_flag, kFaultSoftmax);
