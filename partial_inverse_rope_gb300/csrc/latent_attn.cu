@@ -40,7 +40,7 @@
 //     that it delivers.
 //   bf16, 32 rows of 1 to 16384 tokens: 67.3 us, 4.05 TB/s with start and join, 6.2
 //     in between.
-//   e4m3, 96 rows of 4000 to 20000 tokens: 272 us, 2.6 TB/s, 555 TFLOP/s; 4350
+//   e4m3, 96 rows of 4000 to 20000 tokens: 273 us, 2.5 TB/s, 552 TFLOP/s; 4350
 //     cycles a tile, of which shared memory is busy for 3600: 1540 for the MMAs'
 //     operands, 2050 for codes that land, are read and are written as bf16, and
 //     the rest. Issue slots are 59% busy.
