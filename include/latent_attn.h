@@ -16,8 +16,12 @@
  *   KV_LATENT_E4M3 : nope e4m3 codes, pe bf16 values, ceil(nope/64) scale
  *       bytes, padding to a multiple of 16 bytes (left as it was). A scale byte
  *       b stands for 2^(b-127) and belongs to 64 consecutive channels (fewer
- *       in the last group); a channel's value is code * 2^(b-127), which is
- *       exact in bf16. b = 255 makes its whole group read as NaN.
+ *       in the last group); a channel's value is code * 2^(b-127), rounded
+ *       once to bf16. b = 255 makes its whole group read as NaN.
+ *       kv_latent_write stores scale bytes 7 to 246 and 255, with which values
+ *       are exact in bf16. Rows that another program wrote may hold any byte:
+ *       below 7 a value may round in bf16's subnormals, above 246 it may be an
+ *       infinity, in kv_latent_read and in the attention alike.
  *
  * Common contract, beside that of invrope.h (device pointers of the current
  * device, work enqueued on `stream` only, arguments checked on the host before

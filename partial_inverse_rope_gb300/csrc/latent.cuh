@@ -46,10 +46,11 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// A scale byte as two equal bf16 values 2^(byte-127); 255 gives NaN. (The byte
-// is bf16's exponent field; the writer keeps it within 7..246, or 255.)
+// A scale byte as two equal bf16 values 2^(byte-127); 255 gives NaN. The byte is
+// bf16's exponent field, but for 0: 2^-127 is a subnormal. (The writer keeps it
+// within 7..246, or 255; rows from elsewhere may hold any.)
 __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t byte) {
-  const uint32_t h = byte == 255u ? 0x7FC0u : byte << 7;
+  const uint32_t h = byte == 255u ? 0x7FC0u : byte == 0u ? 0x0040u : byte << 7;
   return h | (h << 16);
 }
 
