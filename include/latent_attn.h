@@ -21,7 +21,11 @@
  *       kv_latent_write stores scale bytes 7 to 246 and 255, with which values
  *       are exact in bf16. Rows that another program wrote may hold any byte:
  *       below 7 a value may round in bf16's subnormals, above 246 it may be an
- *       infinity, in kv_latent_read and in the attention alike.
+ *       infinity, in kv_latent_read and in the attention alike. The codes 0x7F
+ *       and 0xFF, NaN in other uses of e4m3, are no NaN in a row: both calls
+ *       take them as 480 and -480, which follow 448. kv_latent_write stores
+ *       neither; a program that writes rows itself and has a NaN to store has
+ *       the scale byte 255 for it.
  *
  * Common contract, beside that of invrope.h (device pointers of the current
  * device, work enqueued on `stream` only, arguments checked on the host before

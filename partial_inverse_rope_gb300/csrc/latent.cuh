@@ -60,6 +60,9 @@ __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t byte) {
 // power of two twice, is exact. Two codes are put in bytes 1 and 3, with byte 2
 // the copies of the first one's sign: one arithmetic shift by 4 then brings
 // both signs and fields to where bf16 has them, and one mask leaves just those.
+// The codes 0x7F and 0xFF come out as 480 and -480, as the format says: a test for
+// them, 10 instructions for 16 codes, takes 5% of the attention's time (96 rows of
+// 4000 to 20000 tokens: 287 us against 274).
 __device__ __forceinline__ uint32_t prmt_signs(uint32_t w, uint32_t selector) {  // 8 + n: byte n's sign, 8 times
   uint32_t r;
   asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "r"(selector));

@@ -71,3 +71,13 @@ def test_the_least_scale_is_not_zero():
     cache, value = _rows_of(torch.tensor([0x38, 0x7E]), 64)  # 1 and 448
     got = ir.kv_latent_read(cache, torch.arange(2, dtype=torch.int32, device="cuda"), 64, 0).cpu()
     assert got[:, 0].tolist() == [2.0 ** -127, 448 * 2.0 ** -127] == value[:2].tolist()
+
+
+@pytest.mark.parametrize("nope", [64, 128, 400])
+def test_codes_of_all_bits_are_the_numbers_after_the_largest(nope):
+    """0x7F and 0xFF are no NaN in a row: +-480 times the scale, read and attended to."""
+    want, read, attended = _read_and_attended(torch.tensor([0x7F, 0xFF]), nope)
+    byte = torch.arange(256).repeat_interleave(2)
+    want = torch.tensor([480.0, -480.0]).double().repeat(256) * torch.exp2((byte - 127).double())
+    want = torch.where(byte == 255, torch.nan, want).float().to(torch.bfloat16)
+    _same(want[:, None].expand(-1, nope), read, attended)
