@@ -120,7 +120,8 @@ size_t latent_attn_workspace_bytes(int64_t rows, int nh, int64_t max_tokens,
  * larger. Tokens of a page outside [0, num_pages) are left out. A row that
  * attends to nothing gets O = 0 and lse = -inf. Cache rows that are not
  * attended to are not read, so their contents (NaN too) do not matter; an
- * infinity or a NaN in an attended row or in q shows in the heads it reaches.
+ * infinity or a NaN in an attended row or in q shows in the heads it reaches;
+ * a head whose scores are all -inf gets O = NaN and lse = -inf.
  * Scores, sums and accumulators are fp32; the weights are rounded once to
  * bf16 for the second product and O once to bf16. For given arguments and
  * device memory contents the results have the same bits on every call.

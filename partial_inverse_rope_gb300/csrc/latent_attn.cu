@@ -48,6 +48,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 
@@ -433,6 +434,13 @@ __device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp
   return r;
 }
 
+// What a head's accumulators are multiplied by: 0 where nothing was attended to,
+// NaN (0 / 0) where all scores were -inf.
+__device__ __forceinline__ float inverse_of(float sum, float m) {
+  if (sum != 0.f) return 1.f / sum;
+  return m == -INFINITY ? 0.f : NAN;
+}
+
 // (These loads end with their own wait: a register moved or spilled between a
 // load and a wait apart from it would be read too early.)
 // 16 lanes x 64 columns of fp32: thread t holds rows t / 4 (r[4j], r[4j+1]) and
@@ -645,7 +653,11 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
               if (!(bits >> (k & 1) & 1u)) s[4 * u + k] = -INFINITY;
           }
         }
-        float top[2] = {-INFINITY, -INFINITY};
+        // A tile with a token that is attended to has a maximum above -inf even where
+        // all its scores are -inf (their weights are 0 all the same): so m says
+        // whether there was such a token, which a sum of 0 leaves open.
+        const float least = mask != 0 ? -FLT_MAX : -INFINITY;
+        float top[2] = {least, least};
 #pragma unroll
         for (int k = 0; k < 32; ++k) top[(k >> 1) & 1] = fmaxf(top[(k >> 1) & 1], s[k]);
         bool move = false;
@@ -718,7 +730,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
           if (whole) {
             // not for a row without tiles: no barrier of a tile lies between this
             // and another warp's output of the row before, which reads inv
-            if (x.j1 > x.j0) ctl->inv[h] = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+            if (x.j1 > x.j0) ctl->inv[h] = inverse_of(sum[i], m[i]);
             if (p.lse && h < heads)
               p.lse[out + h] = sum[i] == 0.f ? -INFINITY : (m[i] + log2f(sum[i])) * 0.6931471805599453f;
           } else if (h < heads) {
@@ -1175,7 +1187,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) latent_join_kernel(JoinPar
     }
     for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     __syncwarp();
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = inverse_of(sum, top);
     const int64_t out = static_cast<int64_t>(e.y) * p.nh + head;
     // partials k0, k0 + step, ... of channels 128 q + 4 lane and on
     const auto add = [&](float4& acc, int k0, int step, int q) {
