@@ -1339,9 +1339,12 @@ int attend(AttnParams& p, const void* q, void* workspace, size_t workspace_bytes
                       {p.cache, static_cast<size_t>(p.num_slots) * p.l.row_bytes},
                       {p.table, static_cast<size_t>(p.rows) * p.width * 4},
                       {p.lens, p.lens ? static_cast<size_t>(p.rows) * 4 : 0}};
-  Range out[] = {{p.O, vec}, {p.lse, p.lse ? heads * 4 : 0}, {workspace, 0}};
+  // of the workspace, what any device with at least two thread blocks uses; below,
+  // what this one does
+  Range out[] = {{p.O, vec}, {p.lse, p.lse ? heads * 4 : 0},
+                 {workspace, workspace ? make_plan(p.rows, p.nh, max_tokens, p.l.d, 2).bytes : 0}};
   const auto clash = [&] {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       for (const Range& x : in)
         if (overlaps(out[i].at, out[i].bytes, x.at, x.bytes)) return true;
       for (int j = 0; j < i; ++j)
