@@ -380,6 +380,18 @@ def _cache(cache, nope, pe):
     return fmt
 
 
+def _call_device(cache, stream):
+    """The device of a call: the cache's, which has to be the current one (where the
+    library launches) and the stream's."""
+    index = cache.get_device()
+    current = torch.cuda.current_device()
+    if index != current:
+        raise ValueError(f"the tensors are on cuda:{index}, the current device is cuda:{current}")
+    if stream is not None and stream.device_index != index:
+        raise ValueError(f"stream must be of cuda:{index}, got cuda:{stream.device_index}")
+    return index
+
+
 def _same_device(index, **tensors):
     for name, t in tensors.items():
         if t.get_device() != index:
@@ -403,7 +415,7 @@ def kv_latent_write(cache, x, slots, nope: int, pe: int, stream=None):
     n, d = x.shape
     if d != nope + pe or slots.shape[0] != n:
         raise ValueError(f"x must be [n, {nope + pe}] and slots [n]")
-    index = cache.get_device()
+    index = _call_device(cache, stream)
     _same_device(index, x=x, slots=slots)
     pages, size, _ = cache.shape
     st = lib().kv_latent_write(x.data_ptr(), slots.data_ptr(), cache.data_ptr(), n, pages * size, nope, pe, fmt,
@@ -419,7 +431,7 @@ def kv_latent_read(cache, slots, nope: int, pe: int, out=None, stream=None):
     if not (isinstance(slots, torch.Tensor) and _is(slots, torch.int32, 1)):
         _need(slots, "slots", torch.int32, 1)
     n = slots.shape[0]
-    index = cache.get_device()
+    index = _call_device(cache, stream)
     if out is None:
         out = _empty((n, nope + pe), torch.bfloat16, cache.device, stream)
     else:
@@ -441,8 +453,7 @@ def latent_attn_workspace_bytes(rows: int, nh: int, max_tokens: int, nope: int, 
 
 @functools.lru_cache(maxsize=256)
 def _workspace_bytes(index, rows, nh, max_tokens, nope, pe):
-    with torch.cuda.device(index):  # the query goes by the current device's size
-        return latent_attn_workspace_bytes(rows, nh, max_tokens, nope, pe)
+    return latent_attn_workspace_bytes(rows, nh, max_tokens, nope, pe)  # of the current device, `index`
 
 
 def _attn_io(q, cache, nope, pe, max_tokens, O, lse, workspace, stream, **tables):
@@ -453,7 +464,7 @@ def _attn_io(q, cache, nope, pe, max_tokens, O, lse, workspace, stream, **tables
     rows, nh, d = q.shape
     if d != nope + pe:
         raise ValueError(f"q must be [rows, nh, {nope + pe}]")
-    index, device = q.get_device(), q.device
+    index, device = _call_device(cache, stream), cache.device
     if O is None:
         O = _empty((rows, nh, d), torch.bfloat16, device, stream)
     else:
@@ -477,7 +488,7 @@ def _attn_io(q, cache, nope, pe, max_tokens, O, lse, workspace, stream, **tables
     else:
         tables["workspace"] = workspace
         nbytes = workspace.numel() * workspace.element_size()
-    _same_device(index, cache=cache, **tables)
+    _same_device(index, q=q, **tables)
     return fmt, O, lse, (workspace.data_ptr() if workspace is not None else None), nbytes, workspace, \
         _raw_stream(index, stream)
 

@@ -66,3 +66,91 @@ def test_a_workspace_beside_them_is_taken(lib, change):
     if torch.cuda.is_available():
         pytest.skip("the addresses are not real: only for machines without a GPU")
     assert _decode(lib, **change) in (CUDA, DEVICE)
+
+
+class _OnDevice(torch.Tensor):
+    """A host tensor that says it lies on a GPU."""
+    is_cuda = True
+
+    def get_device(self):
+        return self.index
+
+
+def _there(index, *shape, dtype=torch.bfloat16):
+    t = torch.zeros(*shape, dtype=dtype).as_subclass(_OnDevice)
+    t.index = index
+    return t
+
+
+class _Stream:
+    cuda_stream = 0
+
+    def __init__(self, index):
+        self.device_index = index
+
+
+class _Library:
+    """Stands for the library: no entry point may be called but the size queries."""
+
+    def kv_latent_row_bytes(self, nope, pe, fmt):
+        return 2 * (nope + pe)
+
+    def latent_attn_workspace_bytes(self, *_):
+        return 0
+
+
+def _calls(index, other=None, stream=None):
+    """The four calls with their tensors on `index`, and `other` for one in the
+    name's place."""
+    on = lambda name, *shape, **k: _there(other[1] if other and other[0] == name else index, *shape, **k)
+    i32 = torch.int32
+    cache = lambda: on("cache", 4, 16, 64)
+    q = lambda: on("q", 2, 3, 64)
+    out = lambda: {"O": on("O", 2, 3, 64), "lse": on("lse", 2, 3, dtype=torch.float32)}
+    return {
+        "write": lambda: binding.kv_latent_write(cache(), on("x", 2, 64), on("slots", 2, dtype=i32), 48, 16,
+                                                 stream=stream),
+        "read": lambda: binding.kv_latent_read(cache(), on("slots", 2, dtype=i32), 48, 16, out=on("out", 2, 64),
+                                               stream=stream),
+        "decode": lambda: binding.latent_attn_decode(q(), cache(), on("table", 2, 4, dtype=i32),
+                                                     on("lens", 2, dtype=i32), 48, 16, stream=stream, **out()),
+        "sparse": lambda: binding.latent_attn_sparse(q(), cache(), on("table", 2, 4, dtype=i32), 48, 16, stream=stream,
+                                                     **out()),
+    }
+
+
+@pytest.fixture
+def two_devices(monkeypatch):
+    monkeypatch.setattr(binding, "lib", lambda: _Library())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda index: pytest.fail("no call changes the current device"))
+    binding._row_width.cache_clear()
+    binding._workspace_bytes.cache_clear()
+    yield
+    binding._row_width.cache_clear()
+    binding._workspace_bytes.cache_clear()
+
+
+@pytest.mark.parametrize("name", ["write", "read", "decode", "sparse"])
+def test_binding_refuses_tensors_and_streams_of_a_device_that_is_not_current(two_devices, name):
+    with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
+        _calls(1)[name]()
+    with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
+        _calls(1, stream=_Stream(1))[name]()
+    with pytest.raises(ValueError, match="stream must be of cuda:0, got cuda:1"):
+        _calls(0, stream=_Stream(1))[name]()
+
+
+@pytest.mark.parametrize("name,args", [("write", ["cache", "x", "slots"]), ("read", ["cache", "slots", "out"]),
+                                       ("decode", ["cache", "q", "table", "lens", "O", "lse"]),
+                                       ("sparse", ["cache", "q", "table", "O", "lse"])])
+def test_binding_refuses_one_tensor_of_another_device(two_devices, name, args):
+    for arg in args:
+        with pytest.raises(ValueError, match="cuda:"):
+            _calls(0, other=(arg, 1), stream=_Stream(0))[name]()
+
+
+@pytest.mark.parametrize("name", ["write", "read", "decode", "sparse"])
+def test_binding_calls_the_library_with_tensors_of_the_current_device(two_devices, name):
+    with pytest.raises(AttributeError, match=name):  # the stand-in has no entry point
+        _calls(0, stream=_Stream(0))[name]()
