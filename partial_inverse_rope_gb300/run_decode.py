@@ -32,8 +32,10 @@ from . import inputs as W
 
 class Server:
     """A batch of sequences over one layer's cache. Sequence r owns the pages
-    [r * pages, (r + 1) * pages), so its token t has slot r * capacity + t; the
-    caller keeps within ``capacity`` tokens a sequence (lengths are on the device)."""
+    [r * pages, (r + 1) * pages), so its token t has slot r * capacity + t. It holds
+    ``capacity`` tokens: a longer prompt is refused, and in a full sequence the
+    newest token takes the last one's place, at its own position. ``lens`` counts
+    all tokens, on the device, where a replayed graph reads it."""
 
     def __init__(self, rows, capacity, nh, nope, pe, page, fmt, seed=0, device="cuda"):
         pages = -(-capacity // page)
@@ -42,12 +44,18 @@ class Server:
         self.cache = ir.kv_latent_empty(rows * pages, page, nope, pe, fmt, device=device)
         self.table = torch.arange(rows * pages, dtype=torch.int32, device=device).view(rows, pages)
         self.first = torch.arange(rows, dtype=torch.int32, device=device) * self.capacity
-        self.lens = torch.zeros(rows, dtype=torch.int32, device=device)
+        # lengths and the next tokens' slots, with what they stay below, and a copy for a step
+        self.state = torch.stack([torch.zeros_like(self.first), self.first])
+        self.most = torch.stack([torch.full_like(self.first, 2**31 - 2), self.first + (self.capacity - 1)])
+        self.now = self.state.clone()
+        self.lens, self.positions, self.slots = self.state[0], self.now[0], self.now[1]
         self.M = W.postmix_M(nh, seed, device=device)
 
     def prompt(self, x, lens):
         """Vectors ``x`` [sum(lens), d], sequence after sequence."""
-        self.lens.copy_(lens)
+        if int(lens.max()) > self.capacity:
+            raise ValueError(f"a prompt has {int(lens.max())} tokens, a sequence holds {self.capacity}")
+        torch.minimum(torch.stack([lens.int(), self.first + lens.int()]), self.most, out=self.state)
         which = torch.repeat_interleave(torch.arange(self.rows, device=x.device), lens.long())
         begin = torch.cumsum(lens.long(), 0) - lens
         slots = which * self.capacity + torch.arange(len(x), device=x.device) - begin[which]
@@ -63,11 +71,12 @@ class Server:
     def step(self, x, q):
         """One token a sequence: its vector ``x`` [rows, d] and queries ``q``
         [rows, nh, d]; returns the mixed output [rows, nh, d]."""
-        ir.kv_latent_write(self.cache, x, self.first + self.lens, self.nope, self.pe)
-        positions = self.lens.clone()
-        self.lens += 1
+        self.now.copy_(self.state)
+        self.state += 1
+        torch.minimum(self.state, self.most, out=self.state)
+        ir.kv_latent_write(self.cache, x, self.slots, self.nope, self.pe)
         O, _ = ir.latent_attn_decode(q, self.cache, self.table, self.lens, self.nope, self.pe)
-        return ir.invrope_postmix_fwd_ex(O, self.M, self.nope, self.pe, positions=positions)
+        return ir.invrope_postmix_fwd_ex(O, self.M, self.nope, self.pe, positions=self.positions)
 
 
 def main(argv=None):
