@@ -65,3 +65,9 @@ def test_a_prompt_longer_than_a_sequence_is_refused():
     lens = torch.tensor([3, 33], dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError, match="33 tokens"):
         server.prompt(W.normal_bf16((36, D), 1, device="cuda"), lens)
+
+
+@pytest.mark.parametrize("extra", [[], ["--graph"]])
+def test_command_without_steps(extra, capsys):
+    assert run_decode.main(["--rows", "2", "--prompt", "100", "--steps", "0", "--topk", "16"] + extra) == 0
+    assert "finite: True" in capsys.readouterr().out
