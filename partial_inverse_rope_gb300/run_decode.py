@@ -93,6 +93,8 @@ def main(argv=None):
     ap.add_argument("--fmt", choices=["bf16", "e4m3"], default="e4m3")
     ap.add_argument("--graph", action="store_true", help="capture one step and replay it")
     args = ap.parse_args(argv)
+    if args.prompt < 1:
+        ap.error("--prompt must be at least 1: a selected token has to have been written")
 
     dev, d = torch.device("cuda", 0), args.nope + args.pe
     fmt = ir.KV_LATENT_E4M3 if args.fmt == "e4m3" else ir.KV_LATENT_BF16
