@@ -115,7 +115,8 @@ size_t latent_attn_workspace_bytes(int64_t rows, int nh, int64_t max_tokens,
  *      GPU need one each.
  * O, lse and the workspace's bytes that the call needs overlap neither each other
  * nor an input (else INVROPE_ERR_INVALID_ARG).
- * rows >= 0, 1 <= nh <= 128 (above: INVROPE_ERR_UNSUPPORTED), rows * nh < 2^31, scale finite.
+ * rows >= 0, 1 <= nh <= 128 (above: INVROPE_ERR_UNSUPPORTED), rows * nh < 2^31,
+ * scale * log2(e) within fp32's range (else INVROPE_ERR_INVALID_ARG).
  * Several new tokens of one sequence are several rows: repeat its page list
  * and give each its own length.
  * lens[r] is taken as 0 where negative and as max_pages * page_size where

@@ -1301,9 +1301,12 @@ Plan make_plan(int64_t rows, int nh, int64_t max_tokens, int d, int sms) {
   return n;
 }
 
+constexpr double kLog2e = 1.4426950408889634;
+
 // Sizes of a call that are checked before anything else.
 int check_shape(int64_t rows, int nh, int64_t max_tokens, double scale) {
-  if (rows < 0 || nh < 1 || max_tokens < 0 || !std::isfinite(scale)) return INVROPE_ERR_INVALID_ARG;
+  // (the kernel has scale * log2(e) in fp32; NaN fails the comparison too)
+  if (rows < 0 || nh < 1 || max_tokens < 0 || !(std::fabs(scale) * kLog2e <= FLT_MAX)) return INVROPE_ERR_INVALID_ARG;
   if (nh > 128 || rows >= (int64_t(1) << 31) / nh || max_tokens > 0x7FFFFFFF) return INVROPE_ERR_UNSUPPORTED;
   // units of the line, times thread blocks, are 64-bit numbers
   if (rows > 0 && (max_tokens / kTile + 3) > (int64_t(1) << 52) / rows) return INVROPE_ERR_UNSUPPORTED;
@@ -1406,7 +1409,7 @@ AttnParams params(const RowLayout& l, const void* cache, const int32_t* table, c
   p.num_pages = num_pages;
   p.nh = nh;
   p.page_size = page_size;
-  p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  p.scale_log2 = static_cast<float>(scale * kLog2e);
   p.l = l;
   return p;
 }

@@ -68,6 +68,19 @@ def test_a_workspace_beside_them_is_taken(lib, change):
     assert _decode(lib, **change) in (CUDA, DEVICE)
 
 
+@pytest.mark.parametrize("call", [_decode, _sparse])
+@pytest.mark.parametrize("scale,want", [
+    (2.4e38, INVALID), (-2.4e38, INVALID), (1e300, INVALID), (float("nan"), INVALID), (float("-inf"), INVALID),
+    (2.3e38, None), (-2.3e38, None), (1e-320, None), (0.0, None),
+])
+def test_a_scale_beyond_fp32(lib, call, scale, want):
+    """It would make an infinity of every score, and NaN of a score of zero."""
+    if want is None and torch.cuda.is_available():
+        pytest.skip("the addresses are not real: only for machines without a GPU")
+    st = call(lib, scale=scale)
+    assert st == want if want is not None else st in (CUDA, DEVICE)
+
+
 class _OnDevice(torch.Tensor):
     """A host tensor that says it lies on a GPU."""
     is_cuda = True
