@@ -1307,7 +1307,7 @@ constexpr double kLog2e = 1.4426950408889634;
 int check_shape(int64_t rows, int nh, int64_t max_tokens, double scale) {
   // (the kernel has scale * log2(e) in fp32; NaN fails the comparison too)
   if (rows < 0 || nh < 1 || max_tokens < 0 || !(std::fabs(scale) * kLog2e <= FLT_MAX)) return INVROPE_ERR_INVALID_ARG;
-  if (nh > 128 || rows >= (int64_t(1) << 31) / nh || max_tokens > 0x7FFFFFFF) return INVROPE_ERR_UNSUPPORTED;
+  if (nh > 128 || rows > 0x7FFFFFFF / nh || max_tokens > 0x7FFFFFFF) return INVROPE_ERR_UNSUPPORTED;
   // units of the line, times thread blocks, are 64-bit numbers
   if (rows > 0 && (max_tokens / kTile + 3) > (int64_t(1) << 52) / rows) return INVROPE_ERR_UNSUPPORTED;
   return INVROPE_OK;

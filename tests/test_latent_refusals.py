@@ -81,6 +81,15 @@ def test_a_scale_beyond_fp32(lib, call, scale, want):
     assert st == want if want is not None else st in (CUDA, DEVICE)
 
 
+@pytest.mark.parametrize("nh", [1, 3, 64, 127, 128])
+def test_the_most_rows(lib, nh):
+    """rows * nh < 2^31: with the most rows a call gets as far as its addresses."""
+    most = (2**31 - 1) // nh
+    for call in (_decode, _sparse):
+        assert call(lib, rows=most, nh=nh, width=1, q=None) == INVALID
+        assert call(lib, rows=most + 1, nh=nh, width=1, q=None) == UNSUPPORTED
+
+
 class _OnDevice(torch.Tensor):
     """A host tensor that says it lies on a GPU."""
     is_cuda = True
