@@ -1127,7 +1127,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) latent_join_kernel(JoinPar
   __shared__ float4 sums[kJoinWarps][32];
   __shared__ float weight[kJoinWarps][kMaxRuns];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-  ptx::griddep_wait();  // launched early: wait for the partials
+  // Launched early: wait for the partials. (They are read with plain loads: the
+  // read-only path is for what does not change while this kernel runs.)
+  ptx::griddep_wait();
   int n = 0;
   for (int c0 = 0; c0 < p.runs; c0 += 32 * kJoinWarps) {
     const int c = c0 + tid;
@@ -1165,13 +1167,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) latent_join_kernel(JoinPar
     float top = -INFINITY, sum = 0.f;
     if (pieces <= 32) {
       ml[0] = make_float2(-INFINITY, 0.f);
-      if (lane < pieces) ml[0] = __ldg(p.part_ml + slot(lane));
+      if (lane < pieces) ml[0] = p.part_ml[slot(lane)];
       top = ml[0].x;
     } else {
 #pragma unroll
       for (int i = 0; i < kMaxRuns / 32; ++i) {
         ml[i] = make_float2(-INFINITY, 0.f);
-        if (lane + 32 * i < pieces) ml[i] = __ldg(p.part_ml + slot(lane + 32 * i));
+        if (lane + 32 * i < pieces) ml[i] = p.part_ml[slot(lane + 32 * i)];
       }
 #pragma unroll
       for (int i = 0; i < kMaxRuns / 32; ++i) top = fmaxf(top, ml[i].x);
@@ -1196,7 +1198,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) latent_join_kernel(JoinPar
       for (int k = k0; k < pieces; k += step) {
         const float w = weight[warp][k];
         if (c < p.d) {
-          const float4 v = __ldg(reinterpret_cast<const float4*>(p.part + slot(k) * p.d + c));
+          const float4 v = *reinterpret_cast<const float4*>(p.part + slot(k) * p.d + c);
           acc.x += w * v.x;
           acc.y += w * v.y;
           acc.z += w * v.z;
@@ -1235,7 +1237,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) latent_join_kernel(JoinPar
         for (int q = 0; q < kMaxBlocks; ++q) {
           const int c = 128 * q + 4 * lane;
           if (c < p.d) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p.part + slot(k) * p.d + c));
+            const float4 v = *reinterpret_cast<const float4*>(p.part + slot(k) * p.d + c);
             acc[q].x += w * v.x;
             acc[q].y += w * v.y;
             acc[q].z += w * v.z;
