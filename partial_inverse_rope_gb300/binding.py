@@ -384,7 +384,7 @@ def _call_device(cache, stream):
     """The device of a call: the cache's, which has to be the current one (where the
     library launches) and the stream's."""
     index = cache.get_device()
-    current = torch.cuda.current_device()
+    current = torch._C._cuda_getDevice()
     if index != current:
         raise ValueError(f"the tensors are on cuda:{index}, the current device is cuda:{current}")
     if stream is not None and stream.device_index != index:

@@ -144,7 +144,7 @@ def _calls(index, other=None, stream=None):
 @pytest.fixture
 def two_devices(monkeypatch):
     monkeypatch.setattr(binding, "lib", lambda: _Library())
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     monkeypatch.setattr(torch.cuda, "device", lambda index: pytest.fail("no call changes the current device"))
     binding._row_width.cache_clear()
     binding._workspace_bytes.cache_clear()
