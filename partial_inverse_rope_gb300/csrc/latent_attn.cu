@@ -558,7 +558,10 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
   extern __shared__ __align__(1024) char smem[];
   const uint32_t base = ptx::smem_u32(smem);
   if (base & 1023u) {  // never: the declaration asks for it
-    if (threadIdx.x == 0) atomicCAS(&g_latent_fault, 0u, static_cast<unsigned>(kFaultSmem));
+    if (threadIdx.x == 0) {
+      atomicCAS(&g_latent_fault, 0u, static_cast<unsigned>(kFaultSmem));
+      if (p.split) p.split[blockIdx.x] = make_int4(0, 0, 0, 0);  // the join follows what stands there
+    }
     return;
   }
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + kOffCtl);
