@@ -819,7 +819,9 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
       if (!warp_any(x.j1 > x.j0)) continue;
       if (mine == 0) {
         if (item > 0) wait_bar_here(bar(ctl->q_empty), (item - 1) & 1, abort_flag, kFaultScore);
-        if (nblk > kQueryBlocks && ptx::elect_one()) {  // the channels that TMEM has no room for
+        // the channels that TMEM has no room for (after a wait that ran out nothing
+        // is begun that could land when the block has left)
+        if (nblk > kQueryBlocks && !warp_any(*abort_flag != 0) && ptx::elect_one()) {
           ptx::mbar_arrive_expect_tx(bar(ctl->q_full), chunks * p.tile_heads * 128);
           for (int c = 0; c < chunks; ++c)
             ptx::tma_load_3d(base + c * 8192u, &p.tm_q, kQueryBlocks * kBlock + c * 64,
