@@ -10,6 +10,20 @@
 
 #include "latent_attn.h"
 
+// Debug-bounds builds (build.py --debug-bounds) check on the device that indices
+// stay in bounds, and record 0xDB40 | id in the translation unit's fault word
+// where one does not, without trapping.
+#ifdef INVROPE_DEBUG_BOUNDS
+#define LATENT_DBG_CHECK(word, cond, id)                      \
+  do {                                                        \
+    if (!(cond)) atomicCAS(&(word), 0u, 0xDB40u | (id));      \
+  } while (0)
+#else
+#define LATENT_DBG_CHECK(word, cond, id) \
+  do {                                   \
+  } while (0)
+#endif
+
 namespace invrope {
 namespace latent {
 

@@ -217,8 +217,13 @@ __device__ __forceinline__ int load_entry(const int32_t* at) {  // volatile: sta
   return v;
 }
 __device__ __forceinline__ Ref ref_of(const AttnParams& p, int64_t r, int t) {
-  if (!p.lens) return Ref{load_entry(p.table + r * p.width + t), 0};
+  LATENT_DBG_CHECK(g_latent_fault, r >= 0 && r < p.rows && t >= 0, 8);
+  if (!p.lens) {
+    LATENT_DBG_CHECK(g_latent_fault, t < p.width, 9);
+    return Ref{load_entry(p.table + r * p.width + t), 0};
+  }
   const int pg = static_cast<int>(static_cast<unsigned>(t) / static_cast<unsigned>(p.page_size));
+  LATENT_DBG_CHECK(g_latent_fault, pg >= 0 && pg < p.width, 9);
   return Ref{load_entry(p.table + r * p.width + pg), t - pg * p.page_size};
 }
 __device__ __forceinline__ int slot_of(const AttnParams& p, const Ref& x) {
@@ -345,6 +350,7 @@ __device__ __forceinline__ void copy_block(const AttnParams& p, const int (&slot
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const bool there = slot[k] >= 0 && c < p.l.d;
+    LATENT_DBG_CHECK(g_latent_fault, slot[k] < p.num_slots && tok + 2 * k < kTile && (!there || c + 8 <= p.l.d), 10);
     copy_16(unit_addr(stage, tok + 2 * k, unit), from + static_cast<int64_t>(there ? slot[k] : 0) * p.l.row_bytes,
             there);
   }
@@ -372,6 +378,8 @@ __device__ __forceinline__ void copy_codes(const AttnParams& p, const int (&slot
 #pragma unroll
   for (int k = 0; k < kCodeTokens; ++k) {
     const bool there = slot[k] >= 0;
+    LATENT_DBG_CHECK(g_latent_fault,
+                     slot[k] < p.num_slots && c + 16 <= p.l.nope && p.l.scale_off + 16 <= p.l.row_bytes, 11);
     const char* row = p.cache + static_cast<int64_t>(there ? slot[k] : 0) * p.l.row_bytes;
     copy_16(to + k * kCodeStep * 128, row + c, there);
     if (item == 0) copy_16(scales + k * kCodeStep * 128, row + p.l.scale_off, there);  // rows end on 16 bytes
@@ -423,6 +431,10 @@ __device__ __forceinline__ void copy_pe(const AttnParams& p, const int (&slot)[2
 #pragma unroll
   for (int k = 0; k < 2 * kCodeTokens; ++k) {
     const bool there = slot[k] >= 0 && c < p.l.d;
+    LATENT_DBG_CHECK(g_latent_fault,
+                     slot[k] < p.num_slots && tok + 2 + kCodeStep < kTile &&
+                         (!there || p.l.nope + 2 * (c - p.l.nope) + 16 <= p.l.scale_off),
+                     12);
     copy_16(unit_addr(stage, tok + 2 * (k & 1) + kCodeStep * (k >> 1), unit),
             from + static_cast<int64_t>(there ? slot[k] : 0) * p.l.row_bytes, there);
   }
@@ -506,6 +518,7 @@ __device__ __forceinline__ void put_queries(const AttnParams& p, const Piece& x,
   const int h = 16 * quarter + lane / 4;  // and h + 8
   const int chunks = (min(p.l.d, channels) + 63) / 64;
   const int h0 = x.head_tile * p.tile_heads, heads = min(p.tile_heads, p.nh - h0);
+  LATENT_DBG_CHECK(g_latent_fault, x.row >= 0 && x.row < p.rows && heads > 0 && h0 + heads <= p.nh && p.l.d % 8 == 0, 13);
   const __nv_bfloat16* q = p.q + (x.row * p.nh + h0 + h) * p.l.d + 4 * (lane & 3);
   uint32_t r[2][16];
   const auto load = [&](int c0) {
@@ -726,6 +739,10 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
       const bool whole = x.j1 - x.j0 == x.nt;
       const int64_t out = x.row * p.nh + h0;
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (x.j0 > 0 ? 1 : 0);
+      LATENT_DBG_CHECK(g_latent_fault,
+                       x.row >= 0 && x.row < p.rows && heads > 0 && x.j0 >= 0 && x.j1 <= x.nt &&
+                           (whole || (p.part != nullptr && slot < 2 * static_cast<int64_t>(gridDim.x))),
+                       14);
       if ((lane & 3) == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -746,6 +763,10 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
         if (tid == 0) {
           const int64_t first = x.at + kOverhead;
           const int64_t pieces = run_of(first + x.nt - 1, total, nrun) - run_of(first, total, nrun) + 1;
+          LATENT_DBG_CHECK(g_latent_fault,
+                           pieces > 1 && blockIdx.x + pieces <= gridDim.x &&
+                               run_of(first, total, nrun) == static_cast<int64_t>(blockIdx.x),
+                           15);
           p.split[blockIdx.x] = make_int4(static_cast<int>(pieces), static_cast<int>(x.row), x.head_tile, 0);
         }
       }
@@ -840,6 +861,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
           wait_bar_here(bar(ctl->full[s]), phase, abort_flag, kFaultScore);
           ptx::fence_proxy_async_smem();
           ptx::tc_fence_after();
+          LATENT_DBG_CHECK(g_latent_fault, s < kStages && b < kMaxBlocks, 16);
           const uint64_t cd = c_desc + s * (kStageBytes >> 4);
           const bool two = b < nblk - 1 || even;  // 64-channel halves
           if (ptx::elect_one()) {
@@ -896,6 +918,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
         const uint64_t pd = p_desc + (g & 1) * (8192u >> 4);
 #pragma unroll 1
         for (int b = 0; b < nblk; ++b) {
+          LATENT_DBG_CHECK(g_latent_fault, s < kStages && b < kMaxBlocks, 17);
           const uint64_t cd = c_desc + s * (kStageBytes >> 4);
           if (ptx::elect_one()) {
             ptx::tc_mma_ss(b * 64, cd, pd, id_o, !first);
@@ -1000,6 +1023,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
       })) {
         for (int b = 0; b < nblk; ++b) {
           if (!wait_stage()) break;
+          LATENT_DBG_CHECK(g_latent_fault, s < kStages, 18);
           copy_block(p, slot, b, tok, lane, base + kOffRing + s * kStageBytes);
           copies_arrive(bar(ctl->full[s]));
           next_stage();
@@ -1048,6 +1072,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
             ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(ctl->empty[at]), ph, abort_flag, kFaultLoad));
             if (!ok) break;
           }
+          LATENT_DBG_CHECK(g_latent_fault, at < kStages && b < nblk, 18);
           const uint32_t stage = base + kOffRing + at * kStageBytes;
           copy_codes(p, slot, b, item, stage + land(b), stage + land_scales(b));
           if ((b + 1) * kBlock > p.l.nope) {
@@ -1069,6 +1094,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::kThreads, 1) latent_attn_kernel(con
         __syncwarp();  // the scales are another lane's copy
         const int b = 2 * oldest + odd;
         const uint32_t at = s_out + b >= kStages ? s_out + b - kStages : s_out + b;
+        LATENT_DBG_CHECK(g_latent_fault, at < kStages && b < nblk, 19);
         const uint32_t to = base + kOffRing + at * kStageBytes;
         if (b * kBlock < p.l.nope) {
           const bool codes = b * kBlock + 16 * item < p.l.nope;
@@ -1149,8 +1175,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) latent_join_kernel(JoinPar
       n += count[k];
     }
     if (e.x > 0) {
+      LATENT_DBG_CHECK(g_latent_fault, c + e.x <= p.runs && e.x <= kMaxRuns, 20);
       e.w = c;
-      todo[at + __popc(some & ((1u << lane) - 1u))] = e;
+      const int k = at + __popc(some & ((1u << lane) - 1u));
+      LATENT_DBG_CHECK(g_latent_fault, k < kMaxRuns, 21);
+      todo[k] = e;
     }
     __syncthreads();
   }
@@ -1165,6 +1194,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) latent_join_kernel(JoinPar
     const int h = unit % p.tile_heads, head = e.z * p.tile_heads + h;
     const bool live = u < units && head < p.nh;
     const int pieces = live ? e.x : 0;
+    LATENT_DBG_CHECK(g_latent_fault, !live || (pieces > 1 && unit / p.tile_heads < n && e.y >= 0), 22);
     const auto slot = [&](int k) {
       return static_cast<int64_t>(k == 0 ? 2 * e.w : 2 * (e.w + k) + 1) * p.tile_heads + h;
     };
@@ -1423,11 +1453,21 @@ AttnParams params(const RowLayout& l, const void* cache, const int32_t* table, c
 
 }  // namespace
 
+#ifdef INVROPE_DEBUG_BOUNDS
+int take_cache_fault(unsigned int* code);  // latent_cache.cu
+#endif
+
 int take_latent_fault(unsigned int* code) {
   cudaError_t err = cudaMemcpyFromSymbol(code, g_latent_fault, sizeof(*code));
   if (err != cudaSuccess) return cuda_fail(err);
   const unsigned int zero = 0;
   if ((err = cudaMemcpyToSymbol(g_latent_fault, &zero, sizeof(zero))) != cudaSuccess) return cuda_fail(err);
+#ifdef INVROPE_DEBUG_BOUNDS
+  unsigned int cache = 0;
+  const int st = take_cache_fault(&cache);
+  if (st != INVROPE_OK) return st;
+  if (*code == 0) *code = cache;
+#endif
   return INVROPE_OK;
 }
 

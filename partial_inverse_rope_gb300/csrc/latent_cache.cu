@@ -23,6 +23,21 @@
 #include "ptx.cuh"
 
 namespace invrope {
+
+#ifdef INVROPE_DEBUG_BOUNDS
+// The debug-bounds build's fault word of this translation unit (nothing here
+// waits); take_latent_fault() reads and clears it with its own.
+__device__ unsigned int g_cache_fault = 0;
+
+int take_cache_fault(unsigned int* code) {
+  cudaError_t err = cudaMemcpyFromSymbol(code, g_cache_fault, sizeof(*code));
+  if (err != cudaSuccess) return cuda_fail(err);
+  const unsigned int zero = 0;
+  if ((err = cudaMemcpyToSymbol(g_cache_fault, &zero, sizeof(zero))) != cudaSuccess) return cuda_fail(err);
+  return INVROPE_OK;
+}
+#endif
+
 namespace {
 
 using latent::RowLayout;
@@ -66,8 +81,13 @@ __global__ void __launch_bounds__(kThreads)
     for (int r = 0; r < kRows; ++r) {
       const bool ok = one && slot[r] >= 0 && slot[r] < num_slots;
       char* row = cache + static_cast<int64_t>(ok ? slot[r] : 0) * l.row_bytes;
+      LATENT_DBG_CHECK(g_cache_fault, !ok || (slot[r] >= 0 && slot[r] < num_slots && c < l.d), 1);
       if (!E4M3 || c >= l.nope) {
         if (ok) {
+          LATENT_DBG_CHECK(g_cache_fault,
+                           (E4M3 ? l.nope + 2 * (c - l.nope) : 2 * c) + (two ? 32 : 16) <=
+                               (E4M3 ? l.scale_off : l.row_bytes),
+                           2);
           uint4* to = reinterpret_cast<uint4*>(E4M3 ? row + l.nope + 2 * (c - l.nope) : row + 2 * c);
           to[0] = v[r][0];
           if (two) to[1] = v[r][1];
@@ -88,6 +108,7 @@ __global__ void __launch_bounds__(kThreads)
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
       if (!ok || c >= l.nope) continue;
+      LATENT_DBG_CHECK(g_cache_fault, c + 16 <= l.nope && l.scale_off + c / latent::kGroup < l.row_bytes, 3);
       const bool bad = __float_as_uint(amax) == 0x7F800000u;
       const int e = bad ? 0 : scale_exponent(amax);
       const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e
@@ -126,6 +147,8 @@ __global__ void __launch_bounds__(kThreads)
     for (int r = 0; r < kRows; ++r) {
       const bool ok = one && slot[r] >= 0 && slot[r] < num_slots;
       const char* row = cache + static_cast<int64_t>(ok ? slot[r] : 0) * l.row_bytes;
+      LATENT_DBG_CHECK(g_cache_fault,
+                       !ok || (slot[r] < num_slots && at + (codes || !two ? 16 : 32) <= l.row_bytes), 4);
       v[r][0] = ok ? __ldg(reinterpret_cast<const uint4*>(row + at)) : make_uint4(0u, 0u, 0u, 0u);
       v[r][1] = ok && two && !codes ? __ldg(reinterpret_cast<const uint4*>(row + at) + 1) : make_uint4(0u, 0u, 0u, 0u);
       byte[r] = ok && codes
