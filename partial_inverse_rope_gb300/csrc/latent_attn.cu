@@ -1455,6 +1455,33 @@ AttnParams params(const RowLayout& l, const void* cache, const int32_t* table, c
 
 #ifdef INVROPE_DEBUG_BOUNDS
 int take_cache_fault(unsigned int* code);  // latent_cache.cu
+
+namespace {
+
+// One thread waits in each of the ways of the roles for a barrier that nothing
+// arrives on; a second one then finds the abort flag set and does not wait.
+// done[0] counts the waits that came back, done[1] those that said so.
+__global__ void wait_selftest_kernel(int which, int* done) {
+  __shared__ __align__(8) uint64_t never;
+  __shared__ int abort_flag;
+  const uint32_t bar = ptx::smem_u32(&never);
+  ptx::mbar_init(bar, 1);
+  abort_flag = 0;
+  ptx::fence_mbar_init();
+  for (int k = 0; k < 2; ++k) {
+    if (which == 0) {
+      done[1] += wait_bar(bar, 0, &abort_flag, kFaultLoad) ? 0 : 1;
+    } else if (which == 1) {
+      wait_bar_here(bar, 0, &abort_flag, kFaultScore);
+      done[1] += abort_flag;
+    } else if (k == 0) {
+      wait_bar_noabort(bar, 0);
+    }
+    done[0] += 1;
+  }
+}
+
+}  // namespace
 #endif
 
 int take_latent_fault(unsigned int* code) {
@@ -1474,6 +1501,26 @@ int take_latent_fault(unsigned int* code) {
 }  // namespace invrope
 
 using namespace invrope;
+
+#ifdef INVROPE_DEBUG_BOUNDS
+// Test hook of the debug-bounds build: lets a wait of the attention's roles run
+// out (`which`: 0 wait_bar, 1 wait_bar_here, 2 wait_bar_noabort; about 2 s);
+// done[2] as above, in host memory. The fault word then holds the wait's code
+// (none for 2).
+extern "C" int latent_debug_wait(int which, int* done) {
+  if (which < 0 || which > 2 || !done) return INVROPE_ERR_INVALID_ARG;
+  int* d = nullptr;
+  cudaError_t err = cudaMalloc(&d, 2 * sizeof(int));
+  if (err != cudaSuccess) return cuda_fail(err);
+  if ((err = cudaMemset(d, 0, 2 * sizeof(int))) == cudaSuccess) {
+    wait_selftest_kernel<<<1, 1>>>(which, d);
+    if ((err = cudaGetLastError()) == cudaSuccess)
+      err = cudaMemcpy(done, d, 2 * sizeof(int), cudaMemcpyDeviceToHost);
+  }
+  cudaFree(d);
+  return err == cudaSuccess ? INVROPE_OK : cuda_fail(err);
+}
+#endif
 
 extern "C" size_t latent_attn_workspace_bytes(int64_t rows, int nh, int64_t max_tokens, int nope, int pe) {
   RowLayout l;

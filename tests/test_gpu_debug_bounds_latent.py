@@ -1,7 +1,8 @@
 """The latent cache and its attention through the debug-bounds build (see
 ``test_gpu_debug_bounds.py``), in a fresh process: both formats, every block count,
 odd splits, sizes and heads, rows split over blocks and empty ones, pages, slots and
-indices out of range. No index check records a fault code. Needs a GB300."""
+indices out of range. No index check records a fault code. And the attention's
+bounded waits, which run out where nothing arrives. Needs a GB300."""
 
 import os
 import subprocess
@@ -63,3 +64,43 @@ def test_latent_operators_through_the_debug_bounds_build():
                        timeout=600)
     assert r.returncode == 0, r.stdout + r.stderr
     assert "72 latent cases, fault code 0x0" in r.stdout
+
+
+WAITS = textwrap.dedent("""
+    import ctypes, time
+    import torch
+    import partial_inverse_rope_gb300 as ir
+
+    hook = ir.lib().latent_debug_wait
+    hook.argtypes, hook.restype = [ctypes.c_int, ctypes.POINTER(ctypes.c_int)], ctypes.c_int
+
+    cache = ir.kv_latent_empty(40, 64, 448, 64, ir.KV_LATENT_E4M3)
+    x = torch.randn(2560, 512, device="cuda").to(torch.bfloat16)
+    ir.kv_latent_write(cache, x, torch.arange(2560, dtype=torch.int32, device="cuda"), 448, 64)
+    q = torch.randn(2, 64, 512, device="cuda").to(torch.bfloat16)
+    table = torch.arange(40, dtype=torch.int32, device="cuda").view(2, 20).contiguous()
+    lens = torch.tensor([1280, 77], dtype=torch.int32, device="cuda")
+    before = ir.latent_attn_decode(q, cache, table, lens, 448, 64)
+    assert ir.invrope_take_device_fault() == 0
+    for which, code, said in ((0, 0xA01, 2), (1, 0xB01, 2), (2, 0, 0)):
+        done = (ctypes.c_int * 2)()
+        t0 = time.monotonic()
+        assert hook(which, done) == 0
+        took = time.monotonic() - t0
+        assert list(done) == [2, said], (which, list(done))
+        assert 1.5 < took < 4.0, (which, took)  # one wait of 2 s; the second sees the flag
+        assert ir.invrope_take_device_fault() == code, which
+        assert ir.invrope_take_device_fault() == 0
+        after = ir.latent_attn_decode(q, cache, table, lens, 448, 64)
+        assert torch.equal(after[0], before[0]) and torch.equal(after[1], before[1])
+    assert ir.invrope_take_device_fault() == 0
+    print("waits ran out, context usable")
+""")
+
+
+def test_waits_that_run_out_report_and_leave_the_context_usable():
+    lib = build(debug_bounds=True)
+    env = dict(os.environ, INVROPE_LIBRARY=lib)
+    r = subprocess.run([sys.executable, "-c", WAITS], env=env, cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "waits ran out, context usable" in r.stdout
