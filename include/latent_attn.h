@@ -70,7 +70,8 @@ size_t kv_latent_row_bytes(int nope, int pe, int fmt);
  * A group that holds an infinity or a NaN gets the scale byte 255. The pe
  * channels keep their bf16 bits.
  * x     : bf16 [n, d], 16-byte aligned. slots : int32 [n], 4-byte aligned.
- * cache : must overlap neither. n >= 0 (0 enqueues nothing).
+ * cache : must overlap neither. n >= 0 (0 enqueues nothing), below 2^31 (else
+ * INVROPE_ERR_UNSUPPORTED; kv_latent_read too).
  * A slot outside [0, num_slots) stores nothing. Two equal slots in one call
  * leave that row undefined.
  */
@@ -108,7 +109,8 @@ size_t latent_attn_workspace_bytes(int64_t rows, int nh, int64_t max_tokens,
  * q    : bf16 [rows, nh, d], O : bf16 [rows, nh, d], 16-byte aligned.
  * lse  : fp32 [rows, nh] or NULL.
  * page_table : int32 [rows, max_pages]; lens : int32 [rows].
- * cache: num_pages pages of page_size slots; num_pages * page_size < 2^31.
+ * cache: num_pages pages of page_size slots; num_pages * page_size < 2^31 and
+ *      max_pages * page_size < 2^31 (else INVROPE_ERR_UNSUPPORTED).
  * workspace : 16-byte aligned scratch of at least
  *      latent_attn_workspace_bytes(rows, nh, max_pages * page_size, nope, pe)
  *      bytes; its contents on entry do not matter. Calls that overlap on the
@@ -140,7 +142,8 @@ int latent_attn_decode(const void* q, const void* cache, const int32_t* page_tab
  * The same attention over the cache rows that an index table selects: row r
  * attends to slots idx[r, 0..topk-1]. An index outside [0, num_slots) is left
  * out (kv_idx_local_to_global keeps padding negative); one that appears twice
- * counts twice. idx : int32 [rows, topk], 4-byte aligned, topk >= 0.
+ * counts twice. idx : int32 [rows, topk], 4-byte aligned, 0 <= topk < 2^31 (above:
+ * INVROPE_ERR_UNSUPPORTED).
  * workspace : latent_attn_workspace_bytes(rows, nh, topk, nope, pe) bytes.
  * Everything else as in latent_attn_decode.
  */
