@@ -228,7 +228,6 @@ def _pages(st, case, g):
     st["queue"], st["new"] = queue, new
     st["state"] = torch.cat([lens, torch.tensor([head, case["free"]], dtype=torch.int32, device="cuda")])
     st["next"] = torch.empty_like(st["state"])
-    st["room"] = _room(case)
     return st
 
 
@@ -417,7 +416,7 @@ def run(st):
         return ir.rope_apply(st["x"], st["freqs"], st["positions"], amplitude=st["amplitude"], interleaved=case["inter"],
                              inverse=case["back"])
     if case["op"] == "pages":
-        got = ir.kv_pages_advance(st["state"], st["table"], st["queue"], st["new"], case["page"], st["room"],
+        got = ir.kv_pages_advance(st["state"], st["table"], st["queue"], st["new"], case["page"], _room(case),
                                   state_out=st["next"])
         return (*got, st["next"], st["table"], st["queue"])
     if case["op"] == "slots":
