@@ -396,13 +396,17 @@ def kv_latent_row_bytes(nope: int, pe: int, fmt: int) -> int:
 def kv_latent_empty(num_pages: int, page_size: int, nope: int, pe: int, fmt: int = KV_LATENT_BF16, device="cuda"):
     """A cache of ``num_pages`` pages: bf16 ``[num_pages, page_size, nope+pe]``,
     or uint8 ``[num_pages, page_size, row bytes]`` for ``KV_LATENT_E4M3`` and
-    ``KV_LATENT_E2M1``, whose rows' widths tell them apart. Its contents are undefined until they are written."""
+    ``KV_LATENT_E2M1``. Its contents are undefined until they are written. The tensor itself
+    carries its format, its views and copies do not: of those, the width of a row tells it."""
     nbytes = kv_latent_row_bytes(nope, pe, fmt)
     if nbytes == 0:
         raise ValueError(f"no cache row for nope={nope}, pe={pe}, fmt={fmt}")
     if fmt != KV_LATENT_BF16:
-        return torch.empty(num_pages, page_size, nbytes, dtype=torch.uint8, device=device)
-    return torch.empty(num_pages, page_size, nbytes // 2, dtype=torch.bfloat16, device=device)
+        cache = torch.empty(num_pages, page_size, nbytes, dtype=torch.uint8, device=device)
+    else:
+        cache = torch.empty(num_pages, page_size, nbytes // 2, dtype=torch.bfloat16, device=device)
+    cache._kv_latent_fmt = int(fmt)
+    return cache
 
 
 def _is(t, dtype, ndim):
@@ -414,21 +418,36 @@ def _row_width(nope, pe, fmt):
     return kv_latent_row_bytes(nope, pe, fmt) // (2 if fmt == KV_LATENT_BF16 else 1)
 
 
-def _cache(cache, nope, pe):
-    """Check a cache tensor against the channel split; returns its format. The dtype
-    and the width tell it: bf16 rows are the values, uint8 rows the e4m3 layout or the
-    narrower e2m1 one."""
+_FORMATS = {KV_LATENT_BF16: "bf16", KV_LATENT_E4M3: "e4m3", KV_LATENT_E2M1: "e2m1"}
+
+
+def _cache(cache, nope, pe, fmt=None):
+    """Check a cache tensor against the channel split; returns its format: ``fmt``, or what
+    the tensor carries (:func:`kv_latent_empty`), or what dtype and width tell: bf16 rows are
+    the values, uint8 rows the e4m3 layout or the narrower e2m1 one. Widths alone do not tell
+    them apart between splits: 448 + 64 channels in e2m1 are as wide as 224 + 64 in e4m3."""
     if not isinstance(cache, torch.Tensor):
         raise TypeError("cache must be a torch.Tensor")
-    fmt = KV_LATENT_BF16 if cache.dtype is torch.bfloat16 else KV_LATENT_E4M3
-    dtype = torch.uint8 if fmt == KV_LATENT_E4M3 else torch.bfloat16
+    if fmt is not None and fmt not in _FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(_FORMATS)}, got {fmt}")
+    carried = getattr(cache, "_kv_latent_fmt", None)
+    if fmt is None:
+        fmt = carried
+    elif carried is not None and carried != fmt:
+        raise ValueError(f"the cache is {_FORMATS[carried]}, fmt says {_FORMATS[fmt]}")
+    dtype = (torch.bfloat16 if cache.dtype is torch.bfloat16 else torch.uint8) if fmt is None else \
+        (torch.bfloat16 if fmt == KV_LATENT_BF16 else torch.uint8)
     if not _is(cache, dtype, 3):
         _need(cache, "cache", dtype, 3)
-    width = _row_width(nope, pe, fmt)
-    if cache.shape[2] != width and fmt == KV_LATENT_E4M3 and cache.shape[2] == _row_width(nope, pe, KV_LATENT_E2M1):
-        return KV_LATENT_E2M1
+    if fmt is None:
+        fmt = KV_LATENT_BF16 if dtype is torch.bfloat16 else KV_LATENT_E4M3
+        width = _row_width(nope, pe, fmt)
+        if cache.shape[2] != width and fmt == KV_LATENT_E4M3 and cache.shape[2] == _row_width(nope, pe, KV_LATENT_E2M1):
+            return KV_LATENT_E2M1
+    else:
+        width = _row_width(nope, pe, fmt)
     if width and cache.shape[2] != width:  # width 0: the library says why the split is refused
-        raise ValueError(f"cache rows must be {width} wide for nope={nope}, pe={pe}, got {cache.shape[2]}")
+        raise ValueError(f"cache rows must be {width} wide for nope={nope}, pe={pe} in {_FORMATS[fmt]}, got {cache.shape[2]}")
     return fmt
 
 
@@ -455,15 +474,17 @@ def _raw_stream(index, stream):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def kv_latent_write(cache, x, slots, nope: int, pe: int, stream=None):
+def kv_latent_write(cache, x, slots, nope: int, pe: int, stream=None, fmt=None):
     """``cache[slots[i]] = x[i]`` for bf16 vectors ``x`` [n, nope+pe] and int32
     ``slots`` [n] (slot = page * page_size + place in the page), quantising them
-    where the cache has 8 or 4 bits; slots out of range store nothing. Returns ``cache``."""
+    where the cache has 8 or 4 bits; slots out of range store nothing. ``fmt`` says the
+    cache's format where the tensor was not made by :func:`kv_latent_empty` (without it the
+    width of a row does). Returns ``cache``."""
     if stream is None and _calls is not None:
-        got = _calls.latent_write(cache, x, slots, nope, pe)
+        got = _calls.latent_write(cache, x, slots, nope, pe, fmt)
         if got is not None:
             return _made(got, "kv_latent_write")
-    fmt = _cache(cache, nope, pe)
+    fmt = _cache(cache, nope, pe, fmt)
     if not (isinstance(x, torch.Tensor) and _is(x, torch.bfloat16, 2)):
         _need(x, "x", torch.bfloat16, 2)
     if not (isinstance(slots, torch.Tensor) and _is(slots, torch.int32, 1)):
@@ -480,14 +501,14 @@ def kv_latent_write(cache, x, slots, nope: int, pe: int, stream=None):
     return cache
 
 
-def kv_latent_read(cache, slots, nope: int, pe: int, out=None, stream=None):
+def kv_latent_read(cache, slots, nope: int, pe: int, out=None, stream=None, fmt=None):
     """The bf16 vectors [n, nope+pe] that the cache holds at int32 ``slots`` [n]
-    (zeros for a slot out of range)."""
+    (zeros for a slot out of range). ``fmt`` as in :func:`kv_latent_write`."""
     if stream is None and out is None and _calls is not None:
-        got = _calls.latent_read(cache, slots, nope, pe)
+        got = _calls.latent_read(cache, slots, nope, pe, fmt)
         if got is not None:
             return _made(got, "kv_latent_read")
-    fmt = _cache(cache, nope, pe)
+    fmt = _cache(cache, nope, pe, fmt)
     if not (isinstance(slots, torch.Tensor) and _is(slots, torch.int32, 1)):
         _need(slots, "slots", torch.int32, 1)
     n = slots.shape[0]
@@ -524,9 +545,9 @@ def _workspace_bytes(index, rows, nh, max_tokens, nope, pe, fmt):  # of the curr
     return latent_attn_workspace_bytes(rows, nh, max_tokens, nope, pe)
 
 
-def _attn_io(q, cache, nope, pe, max_tokens, O, lse, workspace, stream, **tables):
+def _attn_io(q, cache, nope, pe, max_tokens, O, lse, workspace, stream, fmt, **tables):
     """Checks and outputs common to the two attention calls."""
-    fmt = _cache(cache, nope, pe)
+    fmt = _cache(cache, nope, pe, fmt)
     if not (isinstance(q, torch.Tensor) and _is(q, torch.bfloat16, 3)):
         _need(q, "q", torch.bfloat16, 3)
     rows, nh, d = q.shape
@@ -562,14 +583,14 @@ def _attn_io(q, cache, nope, pe, max_tokens, O, lse, workspace, stream, **tables
 
 
 def latent_attn_decode(q, cache, page_table, lens, nope: int, pe: int, scale=None, O=None, lse=None,
-                       workspace=None, stream=None):
+                       workspace=None, stream=None, fmt=None):
     """Attention of one new token a row over its pages of the latent cache, which
     are keys and values of every head: ``q`` bf16 [rows, nh, nope+pe],
     ``page_table`` int32 [rows, max_pages], ``lens`` int32 [rows] tokens a row.
     ``scale`` defaults to ``(nope+pe) ** -0.5``. Returns ``(O bf16, lse fp32 [rows, nh])``;
-    a row with nothing to attend to gives zeros and -inf."""
+    a row with nothing to attend to gives zeros and -inf. ``fmt`` as in :func:`kv_latent_write`."""
     if stream is None and O is None and lse is None and workspace is None and lens is not None and _calls is not None:
-        got = _calls.attn(q, cache, page_table, lens, nope, pe, scale)
+        got = _calls.attn(q, cache, page_table, lens, nope, pe, scale, fmt)
         if got is not None:
             return _made(got, "latent_attn_decode")
     for t, name, ndim in ((page_table, "page_table", 2), (lens, "lens", 1)):
@@ -577,7 +598,8 @@ def latent_attn_decode(q, cache, page_table, lens, nope: int, pe: int, scale=Non
             _need(t, name, torch.int32, ndim)
     max_pages = page_table.shape[1]
     fmt, O, lse, ws, ws_bytes, workspace, handle = _attn_io(
-        q, cache, nope, pe, max_pages * cache.shape[1], O, lse, workspace, stream, page_table=page_table, lens=lens)
+        q, cache, nope, pe, max_pages * cache.shape[1], O, lse, workspace, stream, fmt, page_table=page_table,
+        lens=lens)
     rows, nh, d = q.shape
     if page_table.shape[0] != rows or lens.shape[0] != rows:
         raise ValueError(f"page_table must be [{rows}, max_pages] and lens [{rows}]")
@@ -589,19 +611,21 @@ def latent_attn_decode(q, cache, page_table, lens, nope: int, pe: int, scale=Non
     return O, lse
 
 
-def latent_attn_sparse(q, cache, idx, nope: int, pe: int, scale=None, O=None, lse=None, workspace=None, stream=None):
+def latent_attn_sparse(q, cache, idx, nope: int, pe: int, scale=None, O=None, lse=None, workspace=None, stream=None,
+                       fmt=None):
     """The same attention over the cache slots that ``idx`` int32 [rows, topk]
     selects for each row (the flat-global table of :func:`kv_idx_local_to_global`;
-    entries out of range, such as -1 padding, are left out)."""
+    entries out of range, such as -1 padding, are left out). ``fmt`` as in
+    :func:`kv_latent_write`."""
     if stream is None and O is None and lse is None and workspace is None and _calls is not None:
-        got = _calls.attn(q, cache, idx, None, nope, pe, scale)
+        got = _calls.attn(q, cache, idx, None, nope, pe, scale, fmt)
         if got is not None:
             return _made(got, "latent_attn_sparse")
     if not (isinstance(idx, torch.Tensor) and _is(idx, torch.int32, 2)):
         _need(idx, "idx", torch.int32, 2)
     rows, topk = idx.shape
     fmt, O, lse, ws, ws_bytes, workspace, handle = _attn_io(
-        q, cache, nope, pe, topk, O, lse, workspace, stream, idx=idx)
+        q, cache, nope, pe, topk, O, lse, workspace, stream, fmt, idx=idx)
     if q.shape[0] != rows:
         raise ValueError("idx must have a row for each of q's")
     nh, d = q.shape[1:]

@@ -225,25 +225,37 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// A cache's format by its type and width, -1 where it has none.
-int format_of(const at::Tensor& cache, int nope, int pe) {
+// A cache's format by its type and width, -1 where it has none, or another than `said` (a
+// number or None) or than the tensor carries (binding.py's kv_latent_empty).
+int format_of(PyObject* o, const at::Tensor& cache, int nope, int pe, PyObject* said) {
   if (!cache.is_cuda() || cache.dim() != 3 || !cache.is_contiguous()) return -1;
   const auto width = static_cast<size_t>(cache.size(2));
   if (width == 0) return -1;
-  if (cache.scalar_type() == at::kBFloat16) return 2 * width == abi.row_bytes(nope, pe, KV_LATENT_BF16) ? KV_LATENT_BF16 : -1;
-  if (cache.scalar_type() != at::kByte) return -1;
-  return width == abi.row_bytes(nope, pe, KV_LATENT_E4M3)   ? KV_LATENT_E4M3
-         : width == abi.row_bytes(nope, pe, KV_LATENT_E2M1) ? KV_LATENT_E2M1
-                                                            : -1;
+  int fmt = -1;
+  if (cache.scalar_type() == at::kBFloat16) {
+    fmt = 2 * width == abi.row_bytes(nope, pe, KV_LATENT_BF16) ? KV_LATENT_BF16 : -1;
+  } else if (cache.scalar_type() == at::kByte) {
+    fmt = width == abi.row_bytes(nope, pe, KV_LATENT_E4M3)   ? KV_LATENT_E4M3
+          : width == abi.row_bytes(nope, pe, KV_LATENT_E2M1) ? KV_LATENT_E2M1
+                                                             : -1;
+  }
+  int v;
+  if (fmt < 0 || (said != Py_None && !(small(said, &v) && v == fmt))) return -1;
+  static PyObject* const name = PyUnicode_InternFromString("_kv_latent_fmt");
+  PyObject* dict = name ? PyObject_GenericGetDict(o, nullptr) : nullptr;
+  PyObject* carried = dict ? PyDict_GetItemWithError(dict, name) : nullptr;  // borrowed
+  if (carried && !(small(carried, &v) && v == fmt)) fmt = -1;
+  Py_XDECREF(dict);
+  return PyErr_Occurred() ? -1 : fmt;
 }
 
-// (cache, x, slots, nope, pe)
+// (cache, x, slots, nope, pe, fmt or None)
 PyObject* latent_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     int nope, pe;
-    if (n != 5 || !small(a[3], &nope) || !small(a[4], &pe) || !THPVariable_Check(a[0])) return not_ordinary();
+    if (n != 6 || !small(a[3], &nope) || !small(a[4], &pe) || !THPVariable_Check(a[0])) return not_ordinary();
     const at::Tensor& cache = THPVariable_Unpack(a[0]);
-    const int fmt = format_of(cache, nope, pe);
+    const int fmt = format_of(a[0], cache, nope, pe, a[5]);
     if (fmt < 0 || !current(&cache)) return not_ordinary();
     const int index = cache.get_device();
     const at::Tensor *x = tensor(a[1], at::kBFloat16, 2, index), *slots = tensor(a[2], at::kInt, 1, index);
@@ -255,13 +267,13 @@ PyObject* latent_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (cache, slots, nope, pe)
+// (cache, slots, nope, pe, fmt or None)
 PyObject* latent_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     int nope, pe;
-    if (n != 4 || !small(a[2], &nope) || !small(a[3], &pe) || !THPVariable_Check(a[0])) return not_ordinary();
+    if (n != 5 || !small(a[2], &nope) || !small(a[3], &pe) || !THPVariable_Check(a[0])) return not_ordinary();
     const at::Tensor& cache = THPVariable_Unpack(a[0]);
-    const int fmt = format_of(cache, nope, pe);
+    const int fmt = format_of(a[0], cache, nope, pe, a[4]);
     if (fmt < 0 || !current(&cache)) return not_ordinary();
     const int index = cache.get_device();
     const at::Tensor* slots = tensor(a[1], at::kInt, 1, index);
@@ -274,16 +286,16 @@ PyObject* latent_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (q, cache, page_table or idx, lens or None, nope, pe, scale or None)
+// (q, cache, page_table or idx, lens or None, nope, pe, scale or None, fmt or None)
 PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     int nope, pe;
     double scale = 0.0;
-    if (n != 7 || !small(a[4], &nope) || !small(a[5], &pe) || (a[6] != Py_None && !real(a[6], &scale)) ||
+    if (n != 8 || !small(a[4], &nope) || !small(a[5], &pe) || (a[6] != Py_None && !real(a[6], &scale)) ||
         !THPVariable_Check(a[1]))
       return not_ordinary();
     const at::Tensor& cache = THPVariable_Unpack(a[1]);
-    const int fmt = format_of(cache, nope, pe);
+    const int fmt = format_of(a[1], cache, nope, pe, a[7]);
     if (fmt < 0 || !current(&cache)) return not_ordinary();
     const int index = cache.get_device();
     const at::Tensor *q = tensor(a[0], at::kBFloat16, 3, index), *table = tensor(a[2], at::kInt, 2, index),
