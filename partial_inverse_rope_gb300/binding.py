@@ -8,7 +8,7 @@ current CUDA stream. All arithmetic runs in the library's kernels. There is no
 fallback: if the library is not built, the first call raises.
 
 Ordinary calls of the serving operators (tensors as they are asked for, outputs
-allocated, the current stream) go through a compiled module, ``_calls.so``, which
+allocated, or given to a step of pages, the current stream) go through a compiled module, ``_calls.so``, which
 leaves all others to the functions here.
 """
 
@@ -670,8 +670,10 @@ def kv_pages_advance(state, page_table, queue, new_tokens, page_size: int, max_t
     tensors of ``out``, if given): the tokens asked for, one sequence after the other, with
     their slots (-1 where the sequence got nothing, and behind the last token), positions
     and sequences, where each sequence's begin, and how many it got."""
-    if stream is None and out is None and _calls is not None:
-        got = _calls.pages_advance(state, page_table, queue, new_tokens, page_size, max_tokens, state_out)
+    if out is not None:
+        out = tuple(out)
+    if stream is None and _calls is not None:
+        got = _calls.pages_advance(state, page_table, queue, new_tokens, page_size, max_tokens, state_out, out)
         if got is not None:
             return _made(got, "kv_pages_advance")
     _int32(state, "state", 1)
@@ -704,7 +706,6 @@ def kv_pages_advance(state, page_table, queue, new_tokens, page_size: int, max_t
             if t.shape[0] != size:
                 raise ValueError(f"{name} must be [{size}]")
             tensors[name] = t
-        out = tuple(out)
     _same_device(index, **tensors)
     slots, positions, rows, starts, granted = out
     st = lib().kv_pages_advance(state.data_ptr(), state_out.data_ptr(), page_table.data_ptr(), queue.data_ptr(),

@@ -1,7 +1,7 @@
 // The binding's ordinary calls, without its Python: arguments are looked at as tensors
 // and handed to the C ABI. Each function returns None where a call is not an ordinary
 // one (a tensor of another type, shape, layout or device than the call takes, a stream
-// or outputs given): binding.py then checks it argument by argument, says what is wrong
+// given, outputs given except to a step of pages): binding.py then checks it argument by argument, says what is wrong
 // or makes the call itself. A status other than INVROPE_OK comes back as a number.
 //
 // A decoding step's calls take the GPU 3 to 5 us each, and took the host 12 to 28 in
@@ -109,12 +109,12 @@ PyObject* guarded(F f) {
   }
 }
 
-// (state, page_table, queue, new_tokens, page_size, max_tokens, state_out or None)
+// (state, page_table, queue, new_tokens, page_size, max_tokens, state_out or None, a tuple of outputs or None)
 PyObject* pages_advance(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     int page_size;
     int64_t room;
-    if (n != 7 || !small(a[4], &page_size) || !number(a[5], &room) || room < 0 || room > 0x7FFFFFFF) return not_ordinary();
+    if (n != 8 || !small(a[4], &page_size) || !number(a[5], &room) || room < 0 || room > 0x7FFFFFFF) return not_ordinary();
     const at::Tensor* state = tensor(a[0], at::kInt, 1, -1);
     if (!state || !current(state)) return not_ordinary();
     const int index = state->get_device();
@@ -124,16 +124,31 @@ PyObject* pages_advance(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!table || !queue || !asked || !out) return not_ordinary();
     const int64_t b = table->size(0);
     if (state->size(0) != b + 2 || out->size(0) != b + 2 || asked->size(0) != b) return not_ordinary();
-    // (one allocation: five took 4 us)
-    const at::Tensor all = ints(*state, {3 * room + 2 * b + 1});
-    const at::Tensor got[5] = {part(all, 0, room), part(all, room, room), part(all, 2 * room, room),
-                               part(all, 3 * room, b + 1), part(all, 3 * room + b + 1, b)};
+    at::Tensor got[5];
+    if (a[7] == Py_None) {
+      // (one allocation: five took 4 us)
+      const at::Tensor all = ints(*state, {3 * room + 2 * b + 1});
+      int64_t offset = 0, k = 0;
+      for (const int64_t size : {room, room, room, b + 1, b}) {
+        got[k++] = part(all, offset, size);
+        offset += size;
+      }
+    } else {
+      if (!PyTuple_Check(a[7]) || PyTuple_GET_SIZE(a[7]) != 5) return not_ordinary();
+      int64_t k = 0;
+      for (const int64_t size : {room, room, room, b + 1, b}) {
+        const at::Tensor* t = tensor(PyTuple_GET_ITEM(a[7], k), at::kInt, 1, index);
+        if (!t || t->size(0) != size) return not_ordinary();
+        got[k++] = *t;
+      }
+    }
     CUstream_st* stream = stream_of(index);
     const int st = unlocked([&] { return abi.pages_advance(data<int32_t>(*state), data<int32_t>(*out), data<int32_t>(*table), data<int32_t>(*queue),
                                      data<int32_t>(*asked), data<int32_t>(got[0]), data<int32_t>(got[1]),
                                      data<int32_t>(got[2]), data<int32_t>(got[3]), data<int32_t>(got[4]), b, table->size(1),
                                      queue->size(0), page_size, room, stream); });
     return done(st, [&] {
+      if (a[7] != Py_None) return Py_NewRef(a[7]);
       PyObject* tuple = PyTuple_New(5);
       for (int k = 0; tuple && k < 5; ++k) PyTuple_SET_ITEM(tuple, k, THPVariable_Wrap(got[k]));
       return tuple;

@@ -88,8 +88,9 @@ class Server:
 
 class PooledServer:
     """A batch of sequences over one layer's cache whose pages are of one pool. A
-    sequence that gets no page keeps its tokens, and its newest one is dropped. All state
-    is on the device, where a replayed graph advances it."""
+    sequence that gets no page keeps its tokens and has not taken the step: ``granted``
+    int32 [rows] says after each step who has (1) and who has not (0). All state is on the
+    device, where a replayed graph advances it, ``granted`` too."""
 
     def __init__(self, rows, capacity, pages, nh, nope, pe, page, fmt, seed=0, device="cuda"):
         self.rows, self.nh, self.nope, self.pe, self.page, self.d = rows, nh, nope, pe, page, nope + pe
@@ -98,6 +99,9 @@ class PooledServer:
         self.lens = self.state[:rows]
         self.freqs, _ = ir.rope_freqs(pe)
         self.one = torch.ones(rows, dtype=torch.int32, device=device)
+        # what a step's call gives: one place for all steps, so that a replayed one's is known
+        self.out = tuple(torch.zeros(n, dtype=torch.int32, device=device) for n in (rows, rows, rows, rows + 1, rows))
+        self.slots, self.positions, _, _, self.granted = self.out
         self.M = W.postmix_M(nh, seed, device=device)
 
     def prompt(self, x, new):
@@ -109,12 +113,15 @@ class PooledServer:
 
     def step(self, x, q):
         """One token a sequence: its vector ``x`` [rows, d] and queries ``q`` [rows, nh, d];
-        returns the mixed output [rows, nh, d]."""
-        slots, positions, _, _, _ = ir.kv_pages_advance(self.state, self.table, self.queue, self.one, self.page, self.rows)
-        q, x = ir.rope_apply([q, x], self.freqs, positions)
-        ir.kv_latent_write(self.cache, x, slots, self.nope, self.pe)
+        returns the mixed output [rows, nh, d]. Where ``granted`` is 0 afterwards the vector is
+        not in the cache and the row of the output answers no query (its place in the sequence
+        is not known to the call, which works at position 0 there): the sequence's step is to be
+        asked for again when others have given pages back."""
+        ir.kv_pages_advance(self.state, self.table, self.queue, self.one, self.page, self.rows, out=self.out)
+        q, x = ir.rope_apply([q, x], self.freqs, self.positions)
+        ir.kv_latent_write(self.cache, x, self.slots, self.nope, self.pe)
         O, _ = ir.latent_attn_decode(q, self.cache, self.table, self.lens, self.nope, self.pe)
-        return ir.invrope_postmix_fwd_ex(O, self.M, self.nope, self.pe, positions=positions)
+        return ir.invrope_postmix_fwd_ex(O, self.M, self.nope, self.pe, positions=self.positions)
 
     def selected(self, q, idx, positions):
         """Queries [rows * chunk, nh, d] over token numbers ``idx`` [rows * chunk, topk] of their
