@@ -18,12 +18,14 @@ table, lengths, slots and positions stay on the device; with --graph a step is
 captured once and replayed.
 
 With --pool the sequences share a pool of pages, three quarters of what they could
-fill: ``kv_pages_advance`` hands out pages, slots and positions and takes pages back
+fill, or what their prompts need where that is more: ``kv_pages_advance`` hands out pages, slots and positions and takes pages back
 when a sequence ends, and ``rope_apply`` turns queries and vectors by their positions,
 in front of what the postmix turns back. Halfway through, and at the end, every fourth
-sequence ends and begins again with a prompt.
+sequence ends and begins again with a prompt. The last line says how many prompts and how
+many of the steps' tokens found no page.
 
-The process exits non-zero if a kernel's watchdog fired.
+The process exits non-zero if a kernel's watchdog fired, an output is not finite, or a
+prompt was refused.
 """
 
 from __future__ import annotations
@@ -131,6 +133,13 @@ class PooledServer:
         return ir.invrope_postmix_fwd_ex(O, self.M, self.nope, self.pe, positions=positions)
 
 
+def pool_pages(lens, most, page):
+    """Pages of a pool for sequences with prompts of these lengths and up to ``most`` tokens:
+    three quarters of what they could fill, and no fewer than the prompts and a first new
+    page of each take."""
+    return max(-(-3 * len(lens) * -(-most // page) // 4), sum(-(-n // page) + 1 for n in lens))
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--rows", type=int, default=8, help="sequences")
@@ -152,15 +161,17 @@ def main(argv=None):
     dev, d = torch.device("cuda", 0), args.nope + args.pe
     fmt = {"bf16": ir.KV_LATENT_BF16, "e4m3": ir.KV_LATENT_E4M3, "e2m1": ir.KV_LATENT_E2M1}[args.fmt]
     most = args.prompt + args.steps + 4
+    lens = torch.linspace(max(1, args.prompt // 2), args.prompt, args.rows, device=dev).int()
     if args.pool:
-        pages = args.rows * -(-most // args.page)
-        server = PooledServer(args.rows, most, max(args.rows * 2, -(-3 * pages // 4)), args.nh, args.nope, args.pe, args.page,
-                              fmt, device=dev)
+        server = PooledServer(args.rows, most, pool_pages(lens.tolist(), most, args.page), args.nh, args.nope, args.pe,
+                              args.page, fmt, device=dev)
     else:
         server = Server(args.rows, most, args.nh, args.nope, args.pe, args.page, fmt, device=dev)
 
-    lens = torch.linspace(max(1, args.prompt // 2), args.prompt, args.rows, device=dev).int()
-    server.prompt(W.normal_bf16((int(lens.sum()), d), 1, device=dev), lens)
+    refused = dropped = 0  # prompts and tokens of steps that found no page
+    taken = server.prompt(W.normal_bf16((int(lens.sum()), d), 1, device=dev), lens)
+    if args.pool:
+        refused += int((taken != lens).sum())
     rows = args.rows * args.chunk
     idx = (torch.rand(rows, args.topk, device=dev) * lens.repeat_interleave(args.chunk)[:, None]).int()
     at = (lens[:, None] - args.chunk + torch.arange(args.chunk, device=dev)).clamp_min(0).int().flatten()
@@ -179,6 +190,7 @@ def main(argv=None):
         step = graph.replay
     us = 0.0
     for part in ((args.steps // 2, args.steps - args.steps // 2) if args.pool else (args.steps,)):
+        before = int(server.lens.sum())
         e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         torch.cuda.synchronize()
         e0.record()
@@ -189,16 +201,19 @@ def main(argv=None):
         torch.cuda.synchronize()
         us += e0.elapsed_time(e1) * 1e3
         if args.pool:
+            dropped += part * args.rows - (int(server.lens.sum()) - before)
             gone = torch.arange(args.rows, device=dev) % 4 == 0
             server.prompt(x[:0], torch.where(gone, -1, 0).int())
-            server.prompt(W.normal_bf16((int(lens[gone].sum()), d), 5, device=dev), torch.where(gone, lens, 0).int())
+            again = torch.where(gone, lens, 0).int()
+            refused += int((server.prompt(W.normal_bf16((int(lens[gone].sum()), d), 5, device=dev), again) != again).sum())
     finite = finite and bool(torch.isfinite(Y).all())
     us /= max(1, args.steps)
     fault = ir.invrope_take_device_fault()
     print(f"{args.rows} sequences of {int(server.lens.min())} to {int(server.lens.max())} tokens, {args.fmt} cache: "
           f"{us:.1f} us a step{' (graph)' if args.graph else ''}; outputs finite: {finite}; "
-          f"watchdog fault code {fault}")
-    return 1 if fault or not finite else 0
+          f"watchdog fault code {fault}"
+          + (f"; no page for {refused} prompts and {dropped} of {args.steps * args.rows} tokens" if args.pool else ""))
+    return 1 if fault or not finite or refused else 0
 
 
 if __name__ == "__main__":
