@@ -6,6 +6,7 @@
 //
 // A decoding step's calls take the GPU 3 to 5 us each, and took the host 12 to 28 in
 // Python, most of it for attributes of tensors and arguments of ctypes.
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
@@ -98,15 +99,13 @@ PyObject* done(int status, F result) {
   return status == INVROPE_OK ? result() : PyLong_FromLong(status);
 }
 
-// C++ exceptions (an allocation that fails) become Python's.
+// C++ exceptions become Python's, as torch's own calls have them: an allocation that fails
+// is torch.OutOfMemoryError.
 template <typename F>
 PyObject* guarded(F f) {
-  try {
-    return f();
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
-  }
+  HANDLE_TH_ERRORS
+  return f();
+  END_HANDLE_TH_ERRORS
 }
 
 // (state, page_table, queue, new_tokens, page_size, max_tokens, state_out or None, a tuple of outputs or None)
