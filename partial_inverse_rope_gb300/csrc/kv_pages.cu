@@ -461,7 +461,8 @@ extern "C" int kv_idx_local_to_slots(const int32_t* idx, const int32_t* page_tab
   // pages open where all blocks are near each other.)
   const int64_t chunks = (p.vectors + kSlotThreads * kStagedPer - 1) / (kSlotThreads * kStagedPer);
   const int64_t grid = static_cast<int64_t>(dev.sms) * 4;
-  if (!seq && max_pages <= kStagedPages && chunks >= 2 * grid && sq * p.per >= 2 * grid * kSlotThreads * kStagedPer) {
+  const int64_t of_sequence = static_cast<int64_t>(p.sq) * p.per;  // (sq itself may be any 64-bit number)
+  if (!seq && max_pages <= kStagedPages && chunks >= 2 * grid && of_sequence >= 2 * grid * kSlotThreads * kStagedPer) {
     const size_t smem = static_cast<size_t>(max_pages) * 4;
     if (four)
       slots_staged_kernel<int4><<<static_cast<unsigned>(grid), kSlotThreads, smem, s>>>(p);
