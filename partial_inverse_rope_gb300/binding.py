@@ -387,10 +387,27 @@ def kv_idx_local_to_global_i64(idx, sq: int, seqlen_kv: int, out=None, stream=No
     return out
 
 
+_C_INTS = ("page_size", "nope", "pe")
+
+
+def _fits(**numbers):
+    """Numbers that go into the library as C ints, which ctypes would cut to 32 or 64 bits."""
+    for name, v in numbers.items():
+        most = 2**31 if name in _C_INTS else 2**63
+        if not -most <= v < most:
+            raise ValueError(f"{name} must be below 2**{most.bit_length() - 1}, got {v}")
+
+
+def _kept(v, bits=32):
+    """A number for the library that keeps it out of range where it is (ctypes would cut it
+    to another one)."""
+    return min(max(int(v), -2**(bits - 1)), 2**(bits - 1) - 1)
+
+
 def kv_latent_row_bytes(nope: int, pe: int, fmt: int) -> int:
     """Bytes of one cache row (0 if the shape is invalid); ``fmt`` is
     ``KV_LATENT_BF16``, ``KV_LATENT_E4M3`` or ``KV_LATENT_E2M1``."""
-    return int(lib().kv_latent_row_bytes(int(nope), int(pe), int(fmt)))
+    return int(lib().kv_latent_row_bytes(_kept(nope), _kept(pe), _kept(fmt)))
 
 
 def kv_latent_empty(num_pages: int, page_size: int, nope: int, pe: int, fmt: int = KV_LATENT_BF16, device="cuda"):
@@ -428,6 +445,7 @@ def _cache(cache, nope, pe, fmt=None):
     them apart between splits: 448 + 64 channels in e2m1 are as wide as 224 + 64 in e4m3."""
     if not isinstance(cache, torch.Tensor):
         raise TypeError("cache must be a torch.Tensor")
+    _fits(nope=nope, pe=pe)
     if fmt is not None and fmt not in _FORMATS:
         raise ValueError(f"fmt must be one of {sorted(_FORMATS)}, got {fmt}")
     carried = getattr(cache, "_kv_latent_fmt", None)
@@ -529,13 +547,14 @@ def kv_latent_read(cache, slots, nope: int, pe: int, out=None, stream=None, fmt=
 
 def latent_attn_workspace_bytes(rows: int, nh: int, max_tokens: int, nope: int, pe: int) -> int:
     """Workspace bytes the attention needs on the current device (0: none)."""
-    return int(lib().latent_attn_workspace_bytes(int(rows), int(nh), int(max_tokens), int(nope), int(pe)))
+    return int(lib().latent_attn_workspace_bytes(_kept(rows, 64), _kept(nh), _kept(max_tokens, 64), _kept(nope), _kept(pe)))
 
 
 def invrope_latent_workspace_bytes(rows: int, nh: int, max_tokens: int, nope: int, pe: int, fmt: int) -> int:
     """Workspace bytes with which the attention over a cache of format ``fmt`` cuts short rows
     the finest: for ``KV_LATENT_E2M1`` more than it asks for."""
-    return int(lib().invrope_latent_workspace_bytes(int(rows), int(nh), int(max_tokens), int(nope), int(pe), int(fmt)))
+    return int(lib().invrope_latent_workspace_bytes(_kept(rows, 64), _kept(nh), _kept(max_tokens, 64), _kept(nope), _kept(pe),
+                                                    _kept(fmt)))
 
 
 @functools.lru_cache(maxsize=256)
@@ -645,14 +664,6 @@ def kv_pages_empty(b: int, max_pages: int, num_pages: int, device="cuda"):
     state[b + 1] = num_pages
     return (state, torch.full((b, max_pages), -1, dtype=torch.int32, device=device),
             torch.arange(num_pages, dtype=torch.int32, device=device))
-
-
-def _fits(**numbers):
-    """Numbers that go into the library as C ints, which ctypes would cut to 32 or 64 bits."""
-    for name, v in numbers.items():
-        most = 2**31 if name == "page_size" else 2**63
-        if not -most <= v < most:
-            raise ValueError(f"{name} must be below 2**{most.bit_length() - 1}, got {v}")
 
 
 def _int32(t, name, ndim):
@@ -765,7 +776,7 @@ def rope_freqs(pe: int, theta: float = 10000.0, scaling: int = ROPE_SCALE_NONE, 
     pe = min(int(pe), 2**31 - 2)
     freqs = torch.empty(pe // 2 if 0 < pe <= 512 else 0, dtype=torch.float64)  # the library says why it refuses others
     amplitude = ctypes.c_double(0.0)
-    st = lib().rope_freqs(max(pe, -1), float(theta), int(scaling), float(factor), float(original), float(beta_fast),
+    st = lib().rope_freqs(max(pe, -1), float(theta), _kept(scaling), float(factor), float(original), float(beta_fast),
                           float(beta_slow), freqs.data_ptr() or None, ctypes.byref(amplitude))
     _check(st, "rope_freqs")
     return freqs, amplitude.value
@@ -842,7 +853,7 @@ def rope_apply(x, freqs, positions=None, pos0: int = 0, offset=None, amplitude: 
             raise ValueError(f"positions must be [{n}]")
         _same_device(index, positions=positions)
         where = positions.data_ptr()
-    st = lib().rope_apply(tensors, len(xs), freqs.data_ptr(), where, int(pos0), n, pe, float(amplitude), dtype, bool(interleaved),
+    st = lib().rope_apply(tensors, len(xs), freqs.data_ptr(), where, int(pos0), n, _kept(pe), float(amplitude), dtype, bool(interleaved),
                           bool(inverse), _raw_stream(index, stream))
     _check(st, "rope_apply")
     return outs if many else outs[0]
