@@ -3,12 +3,14 @@
 // kv_pages_advance: every thread block reads the sequences and adds them up alike, so that
 // no sum goes from one block to another, and then fills a part of the tokens. The state,
 // which may be advanced in place, is written when all have read it: by the one block that
-// a small step is, or by a second launch of one, whose sums are formed while the first
-// one ends. The sums saturate at 2^32 - 1: all they are compared with is below 2^31.
+// a small step is, or by a second launch of one block, which adds up for itself too: it is
+// prepared while the first launch runs and begins when that one's blocks have left. The
+// sums saturate at 2^32 - 1: all they are compared with is below 2^31.
 //
 // A step is bound by its latency: a launch, the sequences, the table or queue entries
 // that depend on them, the tokens' stores. 64 sequences of one token each take 4.8 us;
-// 1000 sequences with 40 prompts, 84000 tokens, 10.8 (by a cluster of 8 blocks 22).
+// 1000 sequences with 40 prompts, 84000 tokens, 10.9 in two launches (by a cluster of 8
+// blocks 22).
 //
 // kv_idx_local_to_slots is one pass over the index table, bound by memory: 65536 x 2048
 // entries 166 us, 6.5 TB/s of the 6.8 of a copy.

@@ -12,7 +12,10 @@
 // which launch and tail are 5; 16384 are written in 8.8 us and read in 9.3 on the
 // GPU alone, with the vectors out of DRAM. 65536 e2m1 rows are read back in 20.0 us (91 MB,
 // 4.6 TB/s; with the 3 blocks a multiprocessor that 78 registers allow 21.9, 2 tokens a
-// thread 21.0, 8 tokens 24.6). A few rows take 4-5 us, one round of
+// thread 21.0, 8 tokens 24.6) and written in 17.7, 131072 in 38.5 and 36.1. What bounds the
+// read there is L1, 77% busy: a warp's store takes 16 of every 32 bytes of 1 KB, so that
+// each sector is stored twice (8.4 million sectors for 134 MB), and the loads of a round wait
+// for its slots; DRAM is 38% busy. The write has issue slots 66% busy, DRAM 47%. A few rows take 4-5 us, one round of
 // dependent reads (slot, row) and a launch.
 //
 // Rounding: a code is rounded once, to nearest even, from x * 2^-e, which is exact

@@ -12,7 +12,13 @@
 // TB/s of the 6.80 of a copy (warps with both kinds of vectors: 367; counters of 4096 rows:
 // DRAM bytes as they should be, issue slots 35% busy); in place, 64 channels of each, 46 us;
 // 10007 rows of 48 heads of 128 fp32 channels 72 us, 6.83 TB/s. 64 rows: 3.1 us, a launch
-// and one round of loads.
+// and one round of loads. What is further from a copy:
+//   - one or two heads in the half layout: 131072 rows of 448 + 64 bf16 channels 56 us, 4.8
+//     TB/s (interleaved 41, 6.5): 90 registers leave 21% of the warps, which wait for their
+//     loads, and DRAM 52% busy (interleaved 51 registers, 42%, 71%).
+//   - vectors of rows whose rotated channels are none: 16384 x 64 heads of 86 + 10 channels 82
+//     us, 4.9 TB/s: issue slots 78% busy, nine loads for each store (partners one by one).
+//   - single channels: 2.3 to 2.6 TB/s: issue slots 84% busy.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
