@@ -8,8 +8,8 @@ current CUDA stream. All arithmetic runs in the library's kernels. There is no
 fallback: if the library is not built, the first call raises.
 
 Ordinary calls of the serving operators (tensors as they are asked for, outputs
-allocated, or given to a step of pages, the current stream) go through a compiled module, ``_calls.so``, which
-leaves all others to the functions here.
+allocated, or given to a step of pages, the current stream) go through a compiled
+module, ``_calls.so``, which leaves all others to the functions here.
 """
 
 from __future__ import annotations

@@ -1,8 +1,8 @@
 // The binding's ordinary calls, without its Python: arguments are looked at as tensors
 // and handed to the C ABI. Each function returns None where a call is not an ordinary
 // one (a tensor of another type, shape, layout or device than the call takes, a stream
-// given, outputs given except to a step of pages): binding.py then checks it argument by argument, says what is wrong
-// or makes the call itself. A status other than INVROPE_OK comes back as a number.
+// given, outputs given except to a step of pages): binding.py then checks it argument by
+// argument, says what is wrong or makes the call itself. A status other than INVROPE_OK comes back as a number.
 //
 // A decoding step's calls take the GPU 3 to 5 us each, and took the host 12 to 28 in
 // Python, most of it for attributes of tensors and arguments of ctypes.
