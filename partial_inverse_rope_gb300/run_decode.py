@@ -20,9 +20,9 @@ captured once and replayed.
 With --pool the sequences share a pool of pages, three quarters of what they could
 fill, or what their prompts need where that is more: ``kv_pages_advance`` hands out
 pages, slots and positions and takes pages back when a sequence ends, and ``rope_apply``
-turns queries and vectors by their positions, in front of what the postmix turns back. Halfway through, and at the end, every fourth
-sequence ends and begins again with a prompt. The last line says how many prompts and how
-many of the steps' tokens found no page.
+turns queries and vectors by their positions, in front of what the postmix turns back.
+Halfway through, and at the end, every fourth sequence ends and begins again with a
+prompt. The last line says how many prompts and how many of the steps' tokens found no page.
 
 The process exits non-zero if a kernel's watchdog fired, an output is not finite, or a
 prompt was refused.
